@@ -294,6 +294,55 @@ lx_status lx_sparse_attn_ws_size(const lx_bhld* Q, double keep, lx_mode mode, si
 lx_status lx_sparse_attn(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, double keep, lx_mode mode,
                          lx_plan* plan, const lx_bhld* O, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- packed sequences
+ * Dense attention over n sequences of different lengths that lie one after the
+ * other in Q, K and V (B = 1, L = all rows), with grouped heads: query head h
+ * reads key/value head h / (Hq / Hkv).  For the text side of the model (prompts,
+ * cross-attention of video tokens to prompts of several lengths), for causal
+ * generation, and for single new tokens over the keys kept so far.
+ *
+ * Sequence i owns the query rows [cu_q[i], cu_q[i+1]) and the key rows
+ * [cu_k[i], cu_k[i] + lk), lk = cu_k[i+1] - cu_k[i], or len_k[i] of them when
+ * len_k is given (slots of a cache that are not full).  With lq query rows, row t
+ * sees the keys u < lk, and with causal != 0 only u <= t + lk - lq (the last
+ * row sees every key; one new token is lq = 1):
+ *   o_t = sum_u p_u v_u / sum_u p_u,  p_u = exp(scale q_t.k_u - max),
+ *   lse_t = log sum_u exp(scale q_t.k_u)      (natural logarithm).
+ * A row that sees no key gives o = 0 and lse = -inf.  Sequences may be empty;
+ * rows before cu_q[0] and from cu_q[n] on are left as they were, and what other
+ * rows or hidden keys hold (infinities and NaN too) does not enter a row. */
+typedef struct lx_pack {
+  const int32_t* cu_q;  /* device [n + 1], ascending, within Q's rows */
+  const int32_t* cu_k;  /* device [n + 1], ascending, within K's rows */
+  const int32_t* len_k; /* device [n], 0 <= len_k[i] <= cu_k[i+1] - cu_k[i], or NULL */
+  int64_t n;            /* sequences, >= 1 */
+} lx_pack;
+
+/* Workspace of lx_attn_packed (0 for prompts that fill the GPU without splitting
+ * their keys; at most 64 MB, or two splits' worth for many rows). */
+lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, size_t* bytes);
+
+/* Q, O [1, Hq, Tq, D]; K, V [1, Hkv, Tk, D], Hq a multiple of Hkv and at most 128
+ * times it; any strides (e.g. the [T, H, D] layout of a projection); scale > 0 and
+ * finite; lse fp32 [Hq, Tq] contiguous or NULL; ws of the size above, 256-byte
+ * aligned (may be NULL for size 0), not shared by calls that may overlap.  The
+ * lengths are read on the device, so a captured call follows them.  A sequence
+ * whose entries do not fit is left out and reported (LX_ERR_PLAN from
+ * lx_last_device_status). */
+lx_status lx_attn_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, const lx_pack* pack, int causal,
+                         float scale, const lx_bhld* O, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace of lx_attn_prefix. */
+lx_status lx_attn_prefix_ws_size(const lx_bhld* Q, size_t* bytes);
+
+/* lx_attn_packed for a batch that shares a prefix: every row sees all keys of Kp, Vp
+ * [1, Hkv, Lp, D] before those of its own sequence.  The prefix is read once for
+ * all sequences; the two parts of a row are joined in fp32.  A sequence may have
+ * no keys of its own. */
+lx_status lx_attn_prefix(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* Vp, const lx_bhld* K, const lx_bhld* V,
+                         const lx_pack* pack, int causal, float scale, const lx_bhld* O, float* lse, void* ws,
+                         size_t ws_bytes, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- NVFP4
  * "Run Wan2.2-A14B on One RTX 5090: 720p Video in 3.8s", §2 (NVFP4
  * quantization-aware training): NVFP4 = E2M1 values, one E4M3 scale per 16

@@ -16,3 +16,4 @@ from .ulysses_ref import (all_to_all_ref, fp8_rows_dequant_ref, fp8_rows_ref, pa
 from .nvfp4_ref import (E2M1_MAX, NVFP4_BLOCK, dequant_nvfp4_ref, e2m1_decode, e2m1_encode,  # noqa: F401
                          e2m1_round, gemm_nvfp4_ref, nvfp4_global_scale, pack_e2m1, quant_nvfp4_ref, sf_tiled,
                          unpack_e2m1)
+from .packed_ref import gemv_nvfp4_ref, packed_attn_bounds, packed_attn_ref  # noqa: F401

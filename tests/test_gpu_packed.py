@@ -1,0 +1,336 @@
+"""Attention over packed sequences and behind a shared prefix (lx_attn_packed,
+lx_attn_prefix) against the fp64 oracle.  The bounds are packed_attn_bounds of
+oracle/packed_ref.py, derived there from the roundings the kernels make."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def lx():
+    import video_dit_dynamic_token_b200 as m
+    return m
+
+
+def _i32(v):
+    return torch.tensor(list(v), dtype=torch.int32, device=DEV)
+
+
+def _cu(lens, start=0):
+    out = [start]
+    for v in lens:
+        out.append(out[-1] + v)
+    return out
+
+
+def _rows(gen, H, T, D, scale=1.0, token_major=True):
+    if token_major:
+        t = (torch.randn((T, H, D), generator=gen) * scale).to(torch.bfloat16).to(DEV)
+        return t.transpose(0, 1).unsqueeze(0)
+    return (torch.randn((1, H, T, D), generator=gen) * scale).to(torch.bfloat16).to(DEV)
+
+
+def _np(t):
+    return t[0].float().cpu().numpy()
+
+
+def _check(got, lse, ref, D, rows=None):
+    o, l = got[0].float().cpu().numpy(), lse.cpu().numpy()
+    live = ~np.isnan(ref["keys"])
+    if rows is not None:
+        live &= rows
+    bo, bl = oracle.packed_attn_bounds(ref, D)
+    fin = live[..., None] & np.isfinite(ref["o"])
+    assert np.isfinite(o[fin]).all()
+    off = np.abs(o - np.where(fin, ref["o"], o))
+    assert np.all(off[fin] <= bo[fin]), f"o: {np.max(off[fin] / bo[fin]):.3g} of the bound"
+    none = live & np.isneginf(ref["lse"])
+    assert np.all(l[none] == -np.inf)
+    ok = live & np.isfinite(ref["lse"])
+    d = np.abs(l[ok] - ref["lse"][ok])
+    assert np.all(d <= bl[ok]), f"lse: {np.max(d / bl[ok]):.3g} of the bound"
+
+
+def _run(lx, lq, lk, hq, hkv, D, causal, seed=0, token_major=True, scale=None, used=None, spare=0, first=0, qs=1.5,
+         prefix=0, ref=True):
+    gen = torch.Generator().manual_seed(seed)
+    Tq, Tk = first + sum(lq) + spare, sum(lk) + spare
+    Q = _rows(gen, hq, max(Tq, 1), D, qs, token_major)
+    K, V = (_rows(gen, hkv, max(Tk, 1), D, 1.0, token_major) for _ in range(2))
+    cq, ck = _cu(lq, first), _cu(lk)
+    out = torch.full_like(Q, 7.0)
+    lse = torch.full((hq, Q.shape[2]), 9.0, device=DEV)
+    lk_t = None if used is None else _i32(used)
+    Kp = Vp = None
+    if prefix:
+        Kp, Vp = (_rows(gen, hkv, prefix, D, 1.0, token_major) for _ in range(2))
+        lx.lx_attn_prefix(Q, Kp, Vp, K, V, _i32(cq), _i32(ck), causal=causal, scale=scale, len_k=lk_t, out=out, lse=lse)
+    else:
+        lx.lx_attn_packed(Q, K, V, _i32(cq), _i32(ck), causal=causal, scale=scale, len_k=lk_t, out=out, lse=lse)
+    assert lx.lx_last_device_status() == 0
+    # rows of no sequence are left as they were
+    for a, b in ((0, first), (cq[-1], Q.shape[2])):
+        assert torch.all(out[:, :, a:b] == 7.0) and torch.all(lse[:, a:b] == 9.0)
+    if not ref:
+        return Q, K, V, out, lse
+    r = oracle.packed_attn_ref(_np(Q), _np(K), _np(V), cq, ck, causal, D ** -0.5 if scale is None else scale, used,
+                               None if Kp is None else _np(Kp), None if Vp is None else _np(Vp))
+    _check(out, lse, r, D)
+    return Q, K, V, out, lse
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_sequence_one_tile(lx, D, causal):
+    _run(lx, [1], [1], 1, 1, D, causal)
+    _run(lx, [5], [5], 2, 1, D, causal)
+    _run(lx, [100], [128], 1, 1, D, causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,D", [(2, 2, 64), (4, 2, 128), (5, 1, 128), (6, 2, 64), (9, 3, 128), (24, 1, 64)])
+def test_ragged_lengths(lx, hq, hkv, D, causal):
+    _run(lx, [1, 17, 64, 130, 3], [1, 17, 64, 130, 3], hq, hkv, D, causal, seed=3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_empty_sequences_and_rows_that_see_nothing(lx, D):
+    # no rows; no keys; more rows than keys under the causal rule (the first rows see nothing)
+    _run(lx, [3, 0, 4, 130, 0, 2], [3, 5, 0, 2, 0, 200], 2, 1, D, True, seed=4, spare=3, first=2)
+    _run(lx, [3, 0, 4, 130, 0, 2], [3, 5, 0, 2, 0, 200], 2, 1, D, False, seed=4, spare=3, first=2)
+
+
+@pytest.mark.parametrize("lk", [1, 127, 128, 129, 255, 257, 700])
+def test_single_token_over_keys(lx, lk):
+    _run(lx, [1, 1, 1], [lk, 1, 3 * lk], 4, 2, 128, True, seed=lk)
+
+
+def test_cache_slots_partly_used(lx):
+    _run(lx, [1, 2, 1, 3], [300, 300, 300, 300], 8, 2, 64, True, seed=6, used=[1, 300, 0, 129])
+
+
+def test_scale_and_layout(lx):
+    _run(lx, [40, 70], [90, 70], 4, 4, 128, True, seed=7, token_major=False, scale=0.02)
+    _run(lx, [40, 70], [90, 70], 4, 4, 64, True, seed=8, scale=1.0, qs=0.3)
+
+
+def test_large_scores_rescale_the_accumulator(lx):
+    """Keys that grow along the sequence make the running maximum jump at every tile."""
+    gen = torch.Generator().manual_seed(9)
+    D, n = 128, 900
+    Q = _rows(gen, 2, n, D)
+    K, V = _rows(gen, 1, n, D), _rows(gen, 1, n, D)
+    K = (K.float() * torch.linspace(0.1, 12, n, device=DEV)[None, None, :, None]).to(torch.bfloat16)
+    for causal in (True, False):
+        lse = torch.empty((2, n), device=DEV)
+        o = lx.lx_attn_packed(Q, K, V, _i32([0, n]), _i32([0, n]), causal=causal, lse=lse)
+        assert lx.lx_last_device_status() == 0
+        _check(o, lse, oracle.packed_attn_ref(_np(Q), _np(K), _np(V), [0, n], [0, n], causal, D ** -0.5), D)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(40, 40, 128), (40, 8, 128), (32, 8, 64)])
+def test_prompts_that_fill_the_gpu(lx, hq, hkv, D):
+    """Enough rows for the two-tile form; checked on sampled heads and rows."""
+    lq = [700, 33, 1500, 257]
+    Q, K, V, out, lse = _run(lx, lq, lq, hq, hkv, D, True, seed=10, spare=5, ref=False)
+    assert lx.lx_attn_packed_ws_size(Q, K, 4) == 0
+    cu = _cu(lq)
+    for h in (0, hq // 2 + 1, hq - 1):
+        g = h // (hq // hkv)
+        r = oracle.packed_attn_ref(_np(Q)[h:h + 1], _np(K)[g:g + 1], _np(V)[g:g + 1], cu, cu, True, D ** -0.5)
+        _check(out[:, h:h + 1], lse[h:h + 1], r, D)
+
+
+def test_two_tile_form_equals_one_tile_form(lx):
+    """The same sequences alone (one row tile, keys split) and in a large pack."""
+    D, hq, hkv = 128, 8, 8
+    lq = [400, 900, 130] * 8
+    Q, K, V, out, lse = _run(lx, lq, lq, hq, hkv, D, True, seed=11, ref=False)
+    assert lx.lx_attn_packed_ws_size(Q, K, len(lq)) == 0
+    cu = _cu(lq)
+    for i in (0, 1, 2, 23):
+        a, b = cu[i], cu[i + 1]
+        l1 = torch.empty((hq, b - a), device=DEV)
+        o1 = lx.lx_attn_packed(Q[:, :, a:b], K[:, :, a:b], V[:, :, a:b], _i32([0, b - a]), _i32([0, b - a]), lse=l1)
+        assert lx.lx_attn_packed_ws_size(Q[:, :, a:b], K[:, :, a:b], 1) > 0
+        assert lx.lx_last_device_status() == 0
+        assert (o1 - out[:, :, a:b]).abs().max() <= 0.02
+        assert (l1 - lse[:, a:b]).abs().max() <= 1e-4
+
+
+# ---------------------------------------------------------------- values in masked places
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("lq", [[60, 150], [1, 1]])
+def test_what_hidden_rows_hold_does_not_enter(lx, bad, lq):
+    """Rows behind each sequence's keys in use, and past the last sequence."""
+    gen = torch.Generator().manual_seed(12)
+    D, used, cap = 128, [150, 201], 256
+    Q, K, V = _rows(gen, 2, sum(lq) + 4, D), _rows(gen, 1, 2 * cap + 9, D), _rows(gen, 1, 2 * cap + 9, D)
+    cq, ck = _cu(lq), [0, cap, 2 * cap]
+    ref = oracle.packed_attn_ref(_np(Q), _np(K), _np(V), cq, ck, True, D ** -0.5, used)
+    for i in range(2):
+        K[:, :, ck[i] + used[i]:ck[i + 1]] = bad
+        V[:, :, ck[i] + used[i]:ck[i + 1]] = bad
+    K[:, :, 2 * cap:] = bad
+    V[:, :, 2 * cap:] = bad
+    Q[:, :, cq[-1]:] = bad
+    lse = torch.zeros((2, Q.shape[2]), device=DEV)
+    o = lx.lx_attn_packed(Q, K, V, _i32(cq), _i32(ck), len_k=_i32(used), lse=lse)
+    assert lx.lx_last_device_status() == 0
+    _check(o, lse, ref, D)
+
+
+@pytest.mark.parametrize("n", [90, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_keys_hidden_by_the_causal_rule_do_not_enter(lx, n, bad):
+    """A non-finite key and value reach the rows that see them and no other."""
+    gen = torch.Generator().manual_seed(13)
+    D = 64
+    Q, K, V = _rows(gen, 2, n, D), _rows(gen, 1, n, D), _rows(gen, 1, n, D)
+    at = n - 25
+    ref = oracle.packed_attn_ref(_np(Q), _np(K), _np(V), [0, n], [0, n], True, D ** -0.5)
+    K[:, :, at] = bad
+    V[:, :, at] = bad
+    lse = torch.empty((2, n), device=DEV)
+    o = lx.lx_attn_packed(Q, K, V, _i32([0, n]), _i32([0, n]), lse=lse)
+    assert lx.lx_last_device_status() == 0
+    rows = np.zeros((2, n), bool)
+    rows[:, :at] = True
+    _check(o, lse, ref, D, rows)
+    assert torch.isnan(o[:, :, at:].float()).all()
+
+
+def test_finite_value_behind_a_non_finite_one(lx):
+    """V alone non-finite and visible: inf where its weight is not zero."""
+    gen = torch.Generator().manual_seed(14)
+    n, D = 140, 128
+    Q, K, V = _rows(gen, 1, n, D), _rows(gen, 1, n, D), _rows(gen, 1, n, D)
+    V[0, 0, 50, 3] = float("inf")
+    o = lx.lx_attn_packed(Q, K, V, _i32([0, n]), _i32([0, n]))
+    assert lx.lx_last_device_status() == 0
+    assert torch.isfinite(o[0, 0, :50].float()).all()
+    assert torch.isinf(o[0, 0, 50:, 3].float()).all() and (o[0, 0, 50:, 3] > 0).all()
+    keep = [c for c in range(D) if c != 3]
+    assert torch.isfinite(o[0, 0, 50:][:, keep].float()).all()
+
+
+# ---------------------------------------------------------------- prefix
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,D", [(2, 2, 64), (5, 1, 128), (8, 2, 128)])
+def test_prefix(lx, hq, hkv, D, causal):
+    _run(lx, [1, 1, 1, 1], [1, 20, 0, 7], hq, hkv, D, causal, seed=20, prefix=200, spare=3)
+    _run(lx, [9, 1, 40, 0, 3], [9, 300, 40, 6, 0], hq, hkv, D, causal, seed=21, prefix=129, first=1)
+    _run(lx, [1], [1], hq, hkv, D, causal, seed=22, prefix=1)
+
+
+def test_prefix_equals_packed_concatenation(lx):
+    gen = torch.Generator().manual_seed(23)
+    hq, hkv, D, Lp = 10, 2, 128, 1000
+    lq, lk = [1, 4, 33], [60, 4, 200]
+    Q = _rows(gen, hq, sum(lq), D)
+    K, V, Kp, Vp = (_rows(gen, hkv, t, D) for t in (sum(lk), sum(lk), Lp, Lp))
+    ck = _cu(lk)
+    cat = lambda P, X: torch.cat([torch.cat((P, X[:, :, ck[i]:ck[i + 1]]), 2) for i in range(3)], 2).contiguous()
+    a = lx.lx_attn_prefix(Q, Kp, Vp, K, V, _i32(_cu(lq)), _i32(ck))
+    b = lx.lx_attn_packed(Q, cat(Kp, K), cat(Vp, V), _i32(_cu(lq)), _i32(_cu([Lp + n for n in lk])))
+    assert lx.lx_last_device_status() == 0
+    assert (a.float() - b.float()).abs().max() <= 0.02
+
+
+# ---------------------------------------------------------------- calls
+def test_many_sequences(lx):
+    """More sequences than threads of a block, some empty."""
+    r = np.random.default_rng(30)
+    lk = r.integers(0, 60, 700).tolist()
+    lq = [min(1, k) for k in lk]
+    _run(lx, lq, lk, 2, 1, 64, True, seed=31)
+    _run(lx, lq, lk, 2, 1, 64, True, seed=32, prefix=77)
+    lq = r.integers(0, 40, 700).tolist()
+    Q, K, V, out, lse = _run(lx, lq, lq, 16, 16, 64, True, seed=33, ref=False)
+    cu = _cu(lq)
+    rr = oracle.packed_attn_ref(_np(Q)[5:6], _np(K)[5:6], _np(V)[5:6], cu, cu, True, 64 ** -0.5)
+    _check(out[:, 5:6], lse[5:6], rr, 64)
+
+
+def test_malformed_lengths_are_reported_and_left_out(lx):
+    from video_dit_dynamic_token_b200._abi import LX_ERR_PLAN
+    gen = torch.Generator().manual_seed(34)
+    Q, K, V = (_rows(gen, 2, 100, 64) for _ in range(3))
+    good = torch.full_like(Q, 3.0)
+    for cq, ck, used in (([0, 50, 40, 100], [0, 50, 60, 100], None), ([0, 50, 80, 101], [0, 50, 60, 100], None),
+                         ([0, 50, 60, 100], [0, 50, -4, 100], None), ([0, 50, 60, 100], [0, 50, 60, 100], [50, 11, 41]),
+                         ([0, 50, 60, 100], [0, 50, 60, 100], [50, 10, -1])):
+        o = good.clone()
+        lx.lx_attn_packed(Q, K, V, _i32(cq), _i32(ck), len_k=None if used is None else _i32(used), out=o)
+        assert lx.lx_last_device_status() == LX_ERR_PLAN
+        assert torch.isfinite(o.float()).all() and not torch.all(o[:, :, :50] == 3.0)
+        o = good.clone()
+        lx.lx_attn_prefix(Q, K, V, K, V, _i32(cq), _i32(ck), len_k=None if used is None else _i32(used), out=o)
+        assert lx.lx_last_device_status() == LX_ERR_PLAN
+    assert lx.lx_last_device_status() == 0
+
+
+def test_captured_call_follows_the_lengths(lx):
+    gen = torch.Generator().manual_seed(35)
+    D, n, cap = 128, 3, 400
+    Q, K, V = _rows(gen, 4, n, D), _rows(gen, 2, n * cap, D), _rows(gen, 2, n * cap, D)
+    cq, ck, used = _i32(range(n + 1)), _i32([0, cap, 2 * cap, 3 * cap]), _i32([1, 1, 1])
+    out, lse = torch.zeros_like(Q), torch.zeros((4, n), device=DEV)
+    ws = torch.empty(lx.lx_attn_packed_ws_size(Q, K, n), dtype=torch.uint8, device=DEV)
+    s = torch.cuda.Stream()
+    call = lambda: lx.lx_attn_packed(Q, K, V, cq, ck, len_k=used, out=out, lse=lse, ws=ws)
+    with torch.cuda.stream(s):
+        call()
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call()
+    for lens in ([1, 1, 1], [400, 17, 128], [3, 0, 399]):
+        used.copy_(torch.tensor(lens, dtype=torch.int32))
+        K.copy_(torch.randn(K.shape, generator=gen).to(torch.bfloat16))
+        ws.fill_(255)
+        g.replay()
+        assert lx.lx_last_device_status() == 0
+        _check(out, lse, oracle.packed_attn_ref(_np(Q), _np(K), _np(V), range(n + 1), ck.tolist(), True, D ** -0.5,
+                                                lens), D)
+
+
+def test_two_streams_and_repeatability(lx):
+    gen = torch.Generator().manual_seed(36)
+    lq = [3, 200, 77]
+    Q, K, V = (_rows(gen, 4, 280, 64) for _ in range(3))
+    cu = _i32(_cu(lq))
+    first = lx.lx_attn_packed(Q, K, V, cu, cu)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(lx.lx_attn_packed(Q, K, V, cu, cu))
+    torch.cuda.synchronize()
+    assert lx.lx_last_device_status() == 0
+    for o in outs:
+        assert torch.equal(o[:, :, :280], first[:, :, :280])
+
+
+def test_rows_far_into_a_long_cache(lx):
+    """Offsets past 2^31 elements: keys of a sequence that lies behind 8.4 M rows."""
+    D, T = 128, 2 ** 23 + 4000
+    K = torch.zeros((1, 2, T, D), dtype=torch.bfloat16, device=DEV)
+    V = torch.zeros((1, 2, T, D), dtype=torch.bfloat16, device=DEV)
+    gen = torch.Generator().manual_seed(37)
+    a, n = T - 1000, 700
+    K[:, :, a:a + n] = _rows(gen, 2, n, D)
+    V[:, :, a:a + n] = _rows(gen, 2, n, D)
+    Q = _rows(gen, 4, 3, D)
+    lse = torch.empty((4, 3), device=DEV)
+    o = lx.lx_attn_packed(Q, K, V, _i32([0, 3]), _i32([a, a + n]), lse=lse)
+    assert lx.lx_last_device_status() == 0
+    _check(o, lse, oracle.packed_attn_ref(_np(Q), _np(K[:, :, a:a + n]), _np(V[:, :, a:a + n]), [0, 3], [0, n], True,
+                                          D ** -0.5), D)

@@ -378,6 +378,74 @@ def lx_sparse_attn(Q, K, V, keep, mode="int8fp8", plan: Plan | None = None, out=
     return out, plan
 
 
+# ---------------------------------------------------------------- packed sequences
+def _pack(cu_q, cu_k, len_k):
+    n = cu_q.numel() - 1
+    for t, m in ((cu_q, n + 1), (cu_k, n + 1), (len_k, n)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != m or not t.is_contiguous()
+                              or not t.is_cuda):
+            raise ValueError("cu_q and cu_k: contiguous int32 CUDA tensors of n + 1 entries, len_k of n")
+    return _abi.LxPack(cu_q.data_ptr(), cu_k.data_ptr(), len_k.data_ptr() if len_k is not None else None, n)
+
+
+def _check_lse(lse, Q):
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (Q.shape[1], Q.shape[2])
+                            or not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous fp32 [Hq, Tq] tensor")
+
+
+def lx_attn_packed_ws_size(Q, K, n) -> int:
+    b = ctypes.c_size_t()
+    q, k = bhld(Q), bhld(K)
+    _check(_abi.load().lx_attn_packed_ws_size(ctypes.byref(q), ctypes.byref(k), int(n), ctypes.byref(b)),
+           "lx_attn_packed_ws_size")
+    return b.value
+
+
+def lx_attn_packed(Q, K, V, cu_q, cu_k, causal=True, scale=None, len_k=None, out=None, lse=None, ws=None,
+                   stream=None):
+    """Attention over packed sequences of different lengths, causal or full, with grouped heads.
+
+    Q: bf16 [1, Hq, Tq, D]; K, V: [1, Hkv, Tk, D]; cu_q, cu_k: int32 [n + 1] starts and ends; len_k: int32 [n]
+    keys in use (caches).  scale None: 1 / sqrt(D).  lse: fp32 [Hq, Tq] to be filled, or None.  Rows outside
+    [cu_q[0], cu_q[n]) of `out` and `lse` are left as they were.  Returns out."""
+    if out is None:
+        out = torch.empty_like(Q)
+    pk = _pack(cu_q, cu_k, len_k)
+    _check_lse(lse, Q)
+    if ws is None:
+        ws = torch.empty(max(lx_attn_packed_ws_size(Q, K, pk.n), 256), dtype=torch.uint8, device=Q.device)
+    q, k, v, o = bhld(Q), bhld(K), bhld(V), bhld(out)
+    scale = Q.shape[-1] ** -0.5 if scale is None else float(scale)
+    _check(_abi.load().lx_attn_packed(ctypes.byref(q), ctypes.byref(k), ctypes.byref(v), ctypes.byref(pk), int(causal),
+                                      scale, ctypes.byref(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "lx_attn_packed")
+    return out
+
+
+def lx_attn_prefix_ws_size(Q) -> int:
+    b = ctypes.c_size_t()
+    q = bhld(Q)
+    _check(_abi.load().lx_attn_prefix_ws_size(ctypes.byref(q), ctypes.byref(b)), "lx_attn_prefix_ws_size")
+    return b.value
+
+
+def lx_attn_prefix(Q, Kp, Vp, K, V, cu_q, cu_k, causal=True, scale=None, len_k=None, out=None, lse=None, ws=None,
+                   stream=None):
+    """lx_attn_packed for a batch whose rows all see the keys Kp, Vp [1, Hkv, Lp, D] before their own."""
+    if out is None:
+        out = torch.empty_like(Q)
+    pk = _pack(cu_q, cu_k, len_k)
+    _check_lse(lse, Q)
+    if ws is None:
+        ws = torch.empty(lx_attn_prefix_ws_size(Q), dtype=torch.uint8, device=Q.device)
+    q, kp, vp, k, v, o = bhld(Q), bhld(Kp), bhld(Vp), bhld(K), bhld(V), bhld(out)
+    scale = Q.shape[-1] ** -0.5 if scale is None else float(scale)
+    _check(_abi.load().lx_attn_prefix(ctypes.byref(q), ctypes.byref(kp), ctypes.byref(vp), ctypes.byref(k),
+                                      ctypes.byref(v), ctypes.byref(pk), int(causal), scale, ctypes.byref(o),
+                                      _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "lx_attn_prefix")
+    return out
+
 
 # ---------------------------------------------------------------- NVFP4
 @dataclass

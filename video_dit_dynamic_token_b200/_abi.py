@@ -39,7 +39,12 @@ class LxRope3d(ctypes.Structure):
                 ("dw", ctypes.c_int32), ("theta", _dbl)]
 
 
+class LxPack(ctypes.Structure):
+    _fields_ = [("cu_q", _vp), ("cu_k", _vp), ("len_k", _vp), ("n", _c_i64)]
+
+
 _P = ctypes.POINTER
+_f32 = ctypes.c_float
 SIGNATURES = {
     "lx_plan_size": [_c_i64, _c_i64, _c_i64, _c_i64, _dbl, _P(_c_i64), _P(_c_sz), _P(_c_sz), _P(_c_sz)],
     "lx_pool_means": [_P(LxBhld), _P(LxBhld), _vp, _vp, _vp],
@@ -63,6 +68,12 @@ SIGNATURES = {
     "lx_sparse_attn_fwd": [_P(LxBhld), _P(LxBhld), _P(LxBhld), _P(LxPlan), ctypes.c_int, _P(LxBhld), _vp, _c_sz, _vp],
     "lx_sparse_attn_ws_size": [_P(LxBhld), _dbl, ctypes.c_int, _P(_c_sz)],
     "lx_sparse_attn": [_P(LxBhld), _P(LxBhld), _P(LxBhld), _dbl, ctypes.c_int, _P(LxPlan), _P(LxBhld), _vp, _c_sz, _vp],
+    "lx_attn_packed_ws_size": [_P(LxBhld), _P(LxBhld), _c_i64, _P(_c_sz)],
+    "lx_attn_packed": [_P(LxBhld), _P(LxBhld), _P(LxBhld), _P(LxPack), ctypes.c_int, _f32, _P(LxBhld), _vp, _vp, _c_sz,
+                       _vp],
+    "lx_attn_prefix_ws_size": [_P(LxBhld), _P(_c_sz)],
+    "lx_attn_prefix": [_P(LxBhld), _P(LxBhld), _P(LxBhld), _P(LxBhld), _P(LxBhld), _P(LxPack), ctypes.c_int, _f32,
+                       _P(LxBhld), _vp, _vp, _c_sz, _vp],
     "lx_ulysses_segment_bytes": [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _P(_c_sz)],
     "lx_ulysses_pack_qkv": [_P(LxBhld), _P(LxBhld), _P(LxBhld), _c_i64, _c_i64, _c_i64, _vp, _vp],
     "lx_ulysses_unpack_qkv": [_vp, _c_i64, _P(LxBhld), _P(LxBhld), _P(LxBhld), _vp],

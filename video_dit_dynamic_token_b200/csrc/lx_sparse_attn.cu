@@ -2,6 +2,7 @@
 // The whole library is this one translation unit (kernels come in as headers).
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -15,6 +16,7 @@
 #include "nvfp4.cuh"
 #include "attn.cuh"
 #include "attn_paired.cuh"
+#include "packed.cuh"
 
 namespace {
 
@@ -345,6 +347,142 @@ bool make_map_codes(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+// ---------------------------------------------------------------- packed sequences
+namespace {
+// Q as (channel, head in group, token, key/value head): one load brings TQ tokens x G heads
+bool make_map_grouped(CUtensorMap* m, const lx_bhld* t, int64_t Hkv, int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int64_t G = t->H / Hkv;
+  const cuuint64_t dims[4] = {(cuuint64_t)t->D, (cuuint64_t)G, (cuuint64_t)t->L, (cuuint64_t)Hkv};
+  const cuuint64_t strides[3] = {(cuuint64_t)(t->sH * 2), (cuuint64_t)(t->sL * 2), (cuuint64_t)(t->sH * G * 2)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)tokens, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline int pack_tokens(int64_t G) { return (int)(128 / G); }
+
+// Prompts run two row tiles per CTA, when there are enough such items for one
+// on every SM and a sequence fills more than one row tile on average; other
+// calls run one row tile per CTA with the keys split.
+bool pack_two_tiles(int64_t Tq, int64_t n, int64_t G, int64_t Hkv) {
+  const int64_t TQ = pack_tokens(G);
+  return Hkv * (Tq / (2 * TQ)) >= lx::kPkSlots / 2 && Tq > n * TQ;
+}
+
+// Room for partial rows: as many splits as 64 MB hold, 2 to 128 (behind a prefix
+// one of its own and one of the sequence's are the least).
+struct PackWs {
+  int64_t splits;
+  size_t ml, part, total;   // [chunk | ml | part]
+};
+PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D) {
+  PackWs w;
+  const int64_t R = Tq * Hq, row = 4 * D + 8;
+  w.splits = std::max<int64_t>(2, std::min<int64_t>(128, ((int64_t)64 << 20) / (R * row)));
+  w.ml = 256;
+  w.part = w.ml + align256((size_t)(w.splits * R * 8));
+  w.total = w.part + align256((size_t)(w.splits * R * D) * 4);
+  return w;
+}
+
+lx_status check_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, const lx_bhld* O) {
+  lx_status st;
+  if ((st = check_bhld(Q)) != LX_OK || (st = check_bhld(K)) != LX_OK || (st = check_bhld(V)) != LX_OK ||
+      (st = check_bhld(O)) != LX_OK)
+    return st;
+  if (!same_shape(K, V) || !same_shape(Q, O) || Q->B != 1 || K->B != 1 || Q->D != K->D || Q->H % K->H != 0)
+    return LX_ERR_INVALID;
+  if (Q->H / K->H > 128 || K->H > 65535) return LX_ERR_UNSUPPORTED;
+  return LX_OK;
+}
+
+template <int D, int NQ>
+lx_status launch_packed(const CUtensorMap* t, const lx::PackParams& p, dim3 grid, cudaStream_t s) {
+  using C = lx::PackCfg<D, NQ>;
+  if (cudaFuncSetAttribute(lx::packed_attn_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+      cudaSuccess)
+    return LX_ERR_CUDA;
+  lx::packed_attn_kernel<D, NQ><<<grid, C::THREADS, C::SMEM, s>>>(t[0], t[1], t[2], t[3], t[4], p);
+  return launch_status();
+}
+
+template <int D>
+lx_status run_packed(const CUtensorMap* t, lx::PackParams p, bool two, cudaStream_t s) {
+  // upper bounds: the lengths are on the device
+  const int64_t rows = two ? 2 * p.TQ : p.TQ;
+  const int64_t tiles = p.Tq / rows + std::min(p.n, p.Tq);
+  if (two) return launch_packed<D, 2>(t, p, dim3((unsigned)tiles, (unsigned)p.Hkv), s);
+  const int64_t prefix = p.Lp ? (p.Tq + rows - 1) / rows : 0;
+  const int64_t items = lx::kPkSlots + (tiles + prefix + 1) * p.Hkv;
+  const int64_t blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
+  if (items > 0x7FFFFFFF || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
+  lx_status st = launch_packed<D, 1>(t, p, dim3((unsigned)items), s);
+  if (st != LX_OK) return st;
+  lx::packed_combine_kernel<D><<<(unsigned)blocks, 256, 0, s>>>(p);
+  return launch_status();
+}
+
+// Both entry points: Kp, Vp null without a prefix.
+lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* Vp, const lx_bhld* K, const lx_bhld* V,
+                           const lx_pack* pack, int causal, float scale, const lx_bhld* O, float* lse, void* ws,
+                           size_t ws_bytes, cudaStream_t s) {
+  lx_status st = check_packed(Q, K, V, O);
+  if (st != LX_OK) return st;
+  if (!pack || !pack->cu_q || !pack->cu_k || pack->n < 1) return LX_ERR_INVALID;
+  if (pack->n > (int64_t)1 << 30) return LX_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return LX_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(pack->cu_q) | reinterpret_cast<uintptr_t>(pack->cu_k) |
+       reinterpret_cast<uintptr_t>(pack->len_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+    return LX_ERR_ALIGN;
+  const int64_t G = Q->H / K->H;
+  const bool two = !Kp && pack_two_tiles(Q->L, pack->n, G, K->H);
+  lx::PackParams p{};
+  if (!two) {
+    const PackWs w = pack_layout(Q->L, Q->H, Q->D);
+    if (!ws || ws_bytes < w.total) return LX_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
+    char* base = reinterpret_cast<char*>(ws);
+    p.chunk = reinterpret_cast<int*>(base);
+    p.ml = reinterpret_cast<float2*>(base + w.ml);
+    p.part = reinterpret_cast<float*>(base + w.part);
+    p.max_np = Kp ? (int)(w.splits / 2) : 0;
+    p.max_ns = (int)(w.splits - p.max_np);
+  }
+  p.cu_q = pack->cu_q;
+  p.cu_k = pack->cu_k;
+  p.len_k = pack->len_k;
+  p.n = (int)pack->n;
+  p.Tq = (int)Q->L;
+  p.Tk = (int)K->L;
+  p.Lp = Kp ? (int)Kp->L : 0;
+  p.G = (int)G;
+  p.Hkv = (int)K->H;
+  p.TQ = pack_tokens(G);
+  p.causal = causal != 0;
+  p.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  p.q = view(Q);
+  p.k = view(K);
+  p.v = view(V);
+  p.o = reinterpret_cast<__nv_bfloat16*>(O->data);
+  p.osH = O->sH;
+  p.osL = O->sL;
+  p.lse = lse;
+  p.limit_ns = kWaitLimitNs;
+  CUtensorMap t[5];
+  const lx_bhld* kv[4] = {K, V, Kp ? Kp : K, Kp ? Vp : V};
+  if (!make_map_grouped(&t[0], Q, K->H, p.TQ)) return LX_ERR_CUDA;
+  for (int i = 0; i < 4; ++i)
+    if (!make_map(&t[1 + i], kv[i]->data, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 1, kv[i]->H, kv[i]->L, kv[i]->D,
+                  kv[i]->sB, kv[i]->sH, kv[i]->sL, 64, lx::kPkKeys))
+      return LX_ERR_CUDA;
+  return Q->D == 128 ? run_packed<128>(t, p, two, s) : run_packed<64>(t, p, two, s);
+}
 }  // namespace
 
 extern "C" {
@@ -774,6 +912,37 @@ lx_status lx_debug_wait_timeout(uint64_t limit_ns, cudaStream_t stream) {
   if (limit_ns == 0 || limit_ns > 10000000000ull) return LX_ERR_INVALID;
   lx::wait_timeout_probe_kernel<<<1, 32, 0, stream>>>((unsigned long long)limit_ns);
   return launch_status();
+}
+
+// ---------------------------------------------------------------- packed sequences
+lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, size_t* bytes) {
+  lx_status st;
+  if ((st = check_packed(Q, K, K, Q)) != LX_OK) return st;
+  if (!bytes || n < 1) return LX_ERR_INVALID;
+  *bytes = pack_two_tiles(Q->L, n, Q->H / K->H, K->H) ? 0 : pack_layout(Q->L, Q->H, Q->D).total;
+  return LX_OK;
+}
+
+lx_status lx_attn_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, const lx_pack* pack, int causal,
+                         float scale, const lx_bhld* O, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return attn_packed_impl(Q, nullptr, nullptr, K, V, pack, causal, scale, O, lse, ws, ws_bytes, stream);
+}
+
+lx_status lx_attn_prefix_ws_size(const lx_bhld* Q, size_t* bytes) {
+  lx_status st = check_bhld(Q);
+  if (st != LX_OK) return st;
+  if (!bytes || Q->B != 1) return LX_ERR_INVALID;
+  *bytes = pack_layout(Q->L, Q->H, Q->D).total;
+  return LX_OK;
+}
+
+lx_status lx_attn_prefix(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* Vp, const lx_bhld* K, const lx_bhld* V,
+                         const lx_pack* pack, int causal, float scale, const lx_bhld* O, float* lse, void* ws,
+                         size_t ws_bytes, cudaStream_t stream) {
+  lx_status st;
+  if ((st = check_bhld(Kp)) != LX_OK || (st = check_bhld(Vp)) != LX_OK || (st = check_bhld(K)) != LX_OK) return st;
+  if (!same_shape(Kp, Vp) || Kp->B != 1 || Kp->H != K->H || Kp->D != K->D) return LX_ERR_INVALID;
+  return attn_packed_impl(Q, Kp, Vp, K, V, pack, causal, scale, O, lse, ws, ws_bytes, stream);
 }
 
 // ---------------------------------------------------------------- Light-Ulysses exchange

@@ -1,0 +1,207 @@
+"""Products of few bf16 rows with NVFP4 weights (lx_nvfp4_gemv) against the fp64
+oracle.
+
+Bound: |Y - y| <= 2^-8 |y| (bf16) + c 2^-23 mag, mag = g sum_k |x_k w_k| + |bias|.
+An fp32 sum passes at most 8 MMA steps of 17 terms in a chunk of 128, K / 128
+chunk additions, 8 splits, the scale and the bias; each of these additions rounds
+(or truncates) once by 2^-23 of a partial sum, which mag bounds: c = 8 * 17 + K / 128
++ 12.  The rounding of x's small elements (2^-39 of a chunk's largest, times the
+largest weight of that row) is added where a test makes it matter."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import nvfp4_ref as nv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def lx():
+    import video_dit_dynamic_token_b200 as m
+    return m
+
+
+def _bf16(a):
+    return torch.from_numpy(np.asarray(a, np.float32)).to(torch.bfloat16).to(DEV)
+
+
+def _weights(lx, rng, N, K, scale=0.05):
+    W = _bf16(rng.standard_normal((N, K)) * scale)
+    return lx.lx_nvfp4_quantize(W), nv.quant_nvfp4_ref(W.float().cpu().numpy())
+
+
+def _bound(ref, K, bias=None):
+    mag = ref["mag"] + (0 if bias is None else np.abs(bias)[None, :])
+    return 2.0 ** -8 * np.abs(ref["y"]) + (8 * 17 + K / 128 + 12) * 2.0 ** -23 * mag + 1e-38
+
+
+def _check(lx, x, wq, wr, bias=None, out=None):
+    K = x.shape[1]
+    y = lx.lx_nvfp4_gemv(x, wq, None if bias is None else torch.from_numpy(bias).to(DEV), out=out)
+    assert lx.lx_last_device_status() == 0
+    ref = oracle.gemv_nvfp4_ref(x.float().cpu().numpy(), wr, bias)
+    off = np.abs(y.float().cpu().numpy() - ref["y"])
+    b = _bound(ref, K, bias)
+    assert np.all(off <= b), f"{np.max(off / b):.3g} of the bound"
+    return y
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16])
+@pytest.mark.parametrize("N,K", [(1, 64), (128, 128), (130, 192), (300, 1088), (77, 4672)])
+def test_shapes(lx, M, N, K):
+    rng = np.random.default_rng(M * 1000 + N + K)
+    wq, wr = _weights(lx, rng, N, K)
+    bias = rng.standard_normal(N).astype(np.float32) if (M + N) % 2 else None
+    _check(lx, _bf16(rng.standard_normal((M, K))), wq, wr, bias)
+
+
+def test_long_k_in_several_segments(lx):
+    """K beyond what one CTA stages at a time (8 splits x 32 chunks of 128)."""
+    rng = np.random.default_rng(1)
+    for M in (1, 16):
+        K = 8 * 32 * 128 + 64 * 77
+        wq, wr = _weights(lx, rng, 130, K)
+        _check(lx, _bf16(rng.standard_normal((M, K))), wq, wr)
+
+
+def test_exact_sums_bit_exact(lx):
+    """Power-of-two scales and small integers make every fp32 sum exact, which pins the
+    place of each code, scale and element of x."""
+    rng = np.random.default_rng(2)
+    N, K = 260, 704
+    for M in (1, 5, 16):
+        codes = rng.integers(0, 16, (N, K)).astype(np.uint8)
+        codes[codes == 8] = 0
+        sf = np.array([0x30, 0x38, 0x40, 0x48], np.uint8)[rng.integers(0, 4, (N, K // 16))]
+        x = rng.integers(-8, 9, (M, K)).astype(np.float32)
+        bias = (rng.integers(-64, 64, N) / 4.0).astype(np.float32)
+        wq = lx.NvFp4Tensor(torch.from_numpy(nv.pack_e2m1(codes)).to(DEV), torch.from_numpy(nv.sf_tiled(sf)).to(DEV),
+                            torch.tensor([0.5], device=DEV), N, K)
+        y = lx.lx_nvfp4_gemv(_bf16(x), wq, torch.from_numpy(bias).to(DEV))
+        ref = oracle.gemv_nvfp4_ref(x, {"codes": codes, "sf": sf, "g": np.float32(0.5)}, bias)
+        assert np.array_equal(y.float().cpu().numpy(), ref["y_bf16"])
+
+
+def test_every_code_and_scale(lx):
+    """One weight row per (code, scale) pair against a single one in x."""
+    codes = np.zeros((127, 64), np.uint8)
+    sf = np.zeros((127, 4), np.uint8)
+    for s in range(127):
+        codes[s, :16] = np.arange(16)
+        sf[s, 0] = s
+    x = np.zeros((16, 64), np.float32)
+    x[np.arange(16), np.arange(16)] = 1
+    wq = lx.NvFp4Tensor(torch.from_numpy(nv.pack_e2m1(codes)).to(DEV), torch.from_numpy(nv.sf_tiled(sf)).to(DEV),
+                        torch.ones(1, device=DEV), 127, 64)
+    y = lx.lx_nvfp4_gemv(_bf16(x), wq)
+    want = nv.e2m1_decode(np.arange(16))[:, None] * oracle.e4m3_decode(np.arange(127))[None, :]
+    assert np.array_equal(y.float().cpu().numpy(), want)      # 6 significant bits: exact in bf16
+
+
+def test_wide_range_of_x(lx):
+    """Rows of very different size, outliers, zeros, and the smallest and largest values."""
+    rng = np.random.default_rng(3)
+    N, K = 200, 512
+    wq, wr = _weights(lx, rng, N, K, scale=1.0)
+    x = rng.standard_normal((12, K))
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    x[2] = 0
+    x[3] *= np.exp(rng.uniform(-15, 15, K))
+    x[4, ::128] = 1e4
+    x[5, 1:] = 0
+    x[6] *= 1e-38                                     # subnormal bf16
+    x[7, 128:] = 0                                    # all-zero chunks
+    xb = _bf16(x)
+    y = lx.lx_nvfp4_gemv(xb, wq)
+    ref = oracle.gemv_nvfp4_ref(xb.float().cpu().numpy(), wr)
+    xf = np.abs(xb.float().cpu().numpy().astype(np.float64)).reshape(12, K // 128, 128)
+    # rounding of elements far below their chunk's largest: 2^-39 of it each
+    wmag = np.abs(nv.dequant_nvfp4_ref(wr["codes"], wr["sf"], wr["g"])).reshape(N, K // 128, 128).sum(-1)
+    small = 2.0 ** -39 * np.einsum("mc,nc->mn", xf.max(-1), wmag)
+    # results near the end of fp32's range: subnormal steps of the sums and of bf16
+    off = np.abs(y.float().cpu().numpy() - ref["y"])
+    assert np.all(off <= _bound(ref, K) + small + 2.0 ** -133 + K * 2.0 ** -149)
+    assert torch.all(y[2] == 0)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_non_finite_x_stays_in_its_row(lx, bad):
+    rng = np.random.default_rng(4)
+    wq, wr = _weights(lx, rng, 150, 256)
+    x = rng.standard_normal((3, 256))
+    clean = oracle.gemv_nvfp4_ref(_bf16(x).float().cpu().numpy(), wr)
+    x[1, 77] = bad
+    y = lx.lx_nvfp4_gemv(_bf16(x), wq).float().cpu().numpy()
+    for m in (0, 2):
+        assert np.all(np.abs(y[m] - clean["y"][m]) <= _bound(clean, 256)[m])
+    want = oracle.gemv_nvfp4_ref(_bf16(x).float().cpu().numpy(), wr)["y"][1]
+    assert np.array_equal(np.isnan(y[1]), np.isnan(want))
+    assert np.array_equal(y[1][~np.isnan(want)], want[~np.isnan(want)])
+
+
+def test_strides_and_untouched_padding(lx):
+    rng = np.random.default_rng(5)
+    N, K = 135, 320
+    wq, wr = _weights(lx, rng, N, K)
+    big = _bf16(rng.standard_normal((4, K + 128)))
+    buf = torch.full((4, N + 6), 5.0, dtype=torch.bfloat16, device=DEV)
+    _check(lx, big[:, 64:64 + K], wq, wr, out=buf[:, 3:3 + N])
+    assert torch.all(buf[:, :3] == 5.0) and torch.all(buf[:, 3 + N:] == 5.0)
+
+
+def test_model_projections_sampled(lx):
+    """The 14B model's widths: modulation (6 x 5120), output projection, second feed-forward product."""
+    for N, K, M in ((30720, 5120, 1), (5120, 5120, 2), (5120, 13824, 16)):
+        gen = torch.Generator(device=DEV).manual_seed(N + K)
+        W = (torch.randn((N, K), device=DEV, generator=gen) * 0.02).to(torch.bfloat16)
+        x = torch.randn((M, K), device=DEV, generator=gen).to(torch.bfloat16)
+        wq = lx.lx_nvfp4_quantize(W)
+        y = lx.lx_nvfp4_gemv(x, wq)
+        rows = np.r_[0, 127, 128, N - 1, np.random.default_rng(N).choice(N, 60, replace=False)]
+        wr = nv.quant_nvfp4_ref(W[torch.from_numpy(rows).to(DEV)].float().cpu().numpy(), wq.gscale.item())
+        ref = oracle.gemv_nvfp4_ref(x.float().cpu().numpy(), wr)
+        assert np.all(np.abs(y.float().cpu().numpy()[:, rows] - ref["y"]) <= _bound(ref, K))
+
+
+def test_equals_the_gemm_on_exact_activations(lx):
+    """Activations that NVFP4 holds exactly: the few-row form and the GEMM agree."""
+    rng = np.random.default_rng(6)
+    N, K, M = 256, 512, 4
+    wq, _ = _weights(lx, rng, N, K)
+    xc = rng.integers(0, 16, (M, K)).astype(np.uint8)
+    xc[xc == 8] = 0
+    sf = np.full((M, K // 16), 0x38, np.uint8)
+    xq = lx.NvFp4Tensor(torch.from_numpy(nv.pack_e2m1(xc)).to(DEV), torch.from_numpy(nv.sf_tiled(sf)).to(DEV),
+                        torch.ones(1, device=DEV), M, K)
+    a, b = lx.lx_nvfp4_gemm(xq, wq).float(), lx.lx_nvfp4_gemv(_bf16(nv.e2m1_decode(xc)), wq).float()
+    assert lx.lx_last_device_status() == 0
+    assert ((a - b).abs() <= 2.0 ** -7 * a.abs() + 1e-3).all()
+
+
+def test_capture_streams_and_repeatability(lx):
+    rng = np.random.default_rng(7)
+    wq, wr = _weights(lx, rng, 500, 1024)
+    x = _bf16(rng.standard_normal((3, 1024)))
+    first = _check(lx, x, wq, wr)
+    out = torch.zeros_like(first)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lx.lx_nvfp4_gemv(x, wq, out=out)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        lx.lx_nvfp4_gemv(x, wq, out=out)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    x.copy_(_bf16(rng.standard_normal((3, 1024))))
+    g.replay()
+    torch.cuda.synchronize()
+    ref = oracle.gemv_nvfp4_ref(x.float().cpu().numpy(), wr)
+    assert np.all(np.abs(out.float().cpu().numpy() - ref["y"]) <= _bound(ref, 1024))

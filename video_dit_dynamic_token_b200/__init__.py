@@ -499,6 +499,26 @@ def lx_nvfp4_gemm(xq: NvFp4Tensor, wq: NvFp4Tensor, bias=None, out=None, stream=
     return out
 
 
+def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, stream=None):
+    """Y = x W^T + bias in bf16 [M, N] for M <= 16 bf16 rows x [M, K] and NVFP4 W [N, K]; bias fp32 [N] or None."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("expected a bf16 [M, K] tensor with contiguous rows")
+    if x.shape[1] != wq.K:
+        raise ValueError("x and W differ in K")
+    M, N = x.shape[0], wq.R
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1:
+        raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
+    if bias is not None and (bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != N):
+        raise ValueError("bias must be a contiguous fp32 tensor of N elements")
+    ldx = x.stride(0) if M > 1 else max(x.stride(0), wq.K)
+    ldy = out.stride(0) if M > 1 else max(out.stride(0), N)
+    _check(_abi.load().lx_nvfp4_gemv(_ptr(x), M, ldx, _ptr(wq.codes), _ptr(wq.sf), _ptr(wq.gscale), _ptr(bias), N,
+                                     wq.K, _ptr(out), ldy, _stream(stream)), "lx_nvfp4_gemv")
+    return out
+
+
 def nvfp4_gemm_flops(M, N, K) -> float:
     return 2.0 * M * N * K
 

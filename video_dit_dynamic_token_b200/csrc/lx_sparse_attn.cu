@@ -14,6 +14,7 @@
 #include "quant.cuh"
 #include "ulysses.cuh"
 #include "nvfp4.cuh"
+#include "nvfp4_gemv.cuh"
 #include "attn.cuh"
 #include "attn_paired.cuh"
 #include "packed.cuh"
@@ -482,6 +483,48 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
                   kv[i]->sB, kv[i]->sH, kv[i]->sL, 64, lx::kPkKeys))
       return LX_ERR_CUDA;
   return Q->D == 128 ? run_packed<128>(t, p, two, s) : run_packed<64>(t, p, two, s);
+}
+// ---------------------------------------------------------------- NVFP4, few rows
+// CTAs per 128-row tile of the weights (a cluster along K).  Cost of a choice: the
+// CTAs of the fullest SM times the chunks of each; of equal ones the most CTAs, which
+// keep more loads in flight.
+int gemv_split(int64_t tiles, int64_t chunks, int sms) {
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= lx::kGvSplit && s <= chunks; ++s) {
+    const int64_t c = ((tiles * s + sms - 1) / sms) * ((chunks + s - 1) / s);
+    if (c <= cost) best = s, cost = c;
+  }
+  return best;
+}
+
+template <int NT>
+lx_status launch_gemv(lx::GemvArgs a, int64_t tiles, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return LX_ERR_CUDA;
+  const int64_t chunks = ((int64_t)a.K + 127) / 128;
+  const int split = gemv_split(tiles, chunks, sms);
+  a.per = (int)((chunks + split - 1) / split);
+  if (tiles * split > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
+  using S = lx::GemvSmem<NT>;
+  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES) !=
+      cudaSuccess)
+    return LX_ERR_CUDA;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = S::BYTES;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<NT>, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
 }
 }  // namespace
 
@@ -1121,6 +1164,30 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
   const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
   lx::nvfp4_gemm_kernel<<<grid, lx::kNvThreads, lx::kNvSmemBytes, stream>>>(ta, tw, a);
   return launch_status();
+}
+
+lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc, const uint8_t* wsf, const float* gw,
+                        const float* bias, int64_t N, int64_t K, void* y, int64_t ldy, cudaStream_t stream) {
+  if (!x || !wc || !wsf || !gw || !y) return LX_ERR_INVALID;
+  if (M < 1 || N < 1 || K < 64 || K % 64 != 0 || K > ((int64_t)1 << 30) || ldx < K || ldy < N) return LX_ERR_INVALID;
+  if (M > lx::kGvMaxRows || N > ((int64_t)1 << 31) - 256) return LX_ERR_UNSUPPORTED;
+  if (!al16(x) || ldx % 8 != 0 || !al16(wc) || !al16(wsf) || (reinterpret_cast<uintptr_t>(y) & 1u) ||
+      ((reinterpret_cast<uintptr_t>(gw) | reinterpret_cast<uintptr_t>(bias)) & 3u))
+    return LX_ERR_ALIGN;
+  lx::GemvArgs a{};
+  a.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  a.wc = wc;
+  a.wsf = wsf;
+  a.gw = gw;
+  a.bias = bias;
+  a.y = reinterpret_cast<__nv_bfloat16*>(y);
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.N = N;
+  a.M = (int)M;
+  a.K = (int)K;
+  const int64_t tiles = (N + 127) / 128;
+  return M <= 8 ? launch_gemv<1>(a, tiles, stream) : launch_gemv<2>(a, tiles, stream);
 }
 
 }  // extern "C"

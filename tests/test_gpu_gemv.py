@@ -1,12 +1,14 @@
 """Products of few bf16 rows with NVFP4 weights (lx_nvfp4_gemv) against the fp64
 oracle.
 
-Bound: |Y - y| <= 2^-8 |y| (bf16) + c 2^-23 mag, mag = g sum_k |x_k w_k| + |bias|.
-An fp32 sum passes at most 8 MMA steps of 17 terms in a chunk of 128, K / 128
-chunk additions, 8 splits, the scale and the bias; each of these additions rounds
-(or truncates) once by 2^-23 of a partial sum, which mag bounds: c = 8 * 17 + K / 128
-+ 12.  The rounding of x's small elements (2^-39 of a chunk's largest, times the
-largest weight of that row) is added where a test makes it matter."""
+Bound: |Y - y| <= 2^-8 |y| (bf16) + c 2^-23 (4 mag + |bias|) + r, mag = g sum_k |x_k w_k|.
+A digit column is an fp32 sum over MMA steps of 64 products; a step adds its products
+with at most 7 roundings (or truncations) of 2^-23 of what is summed and one into the
+column: 8 K / 64.  Eight columns (7 FMAs), 2 powers of two, 8 splits, the scale and
+the bias follow: c = K / 8 + 20.  The magnitudes of the digits of an element add up to
+less than 4 of its own (11 / 3 for a 1 above digits of -4).  r: elements of x
+below 2^-14 of their block's largest are rounded by 2^-22 of it (2^-39 of the row's
+largest if that is more), times the block's weights."""
 import numpy as np
 import pytest
 import torch
@@ -34,15 +36,29 @@ def _weights(lx, rng, N, K, scale=0.05):
 
 
 def _bound(ref, K, bias=None):
-    mag = ref["mag"] + (0 if bias is None else np.abs(bias)[None, :])
-    return 2.0 ** -8 * np.abs(ref["y"]) + (8 * 17 + K / 128 + 12) * 2.0 ** -23 * mag + 1e-38
+    mag = 4 * ref["mag"] + (0 if bias is None else np.abs(bias)[None, :])
+    return 2.0 ** -8 * np.abs(ref["y"]) + (K / 8 + 20) * 2.0 ** -23 * mag + ref["small"] + 1e-38
+
+
+def _ref(x, wr, bias=None):
+    """The oracle's result with the bound r of the rounding of x's small elements."""
+    x = np.asarray(x, np.float64)
+    ref = oracle.gemv_nvfp4_ref(x, wr, bias)
+    M, K = x.shape
+    a = np.abs(np.where(np.isfinite(x), x, 0)).reshape(M, K // 16, 16)
+    top = a.max(-1)
+    lsb = np.maximum(2.0 ** -22 * top, 2.0 ** -39 * top.max(-1, keepdims=True))
+    hit = (a < 2.0 ** -14 * np.maximum(top, 2.0 ** -17 * top.max(-1, keepdims=True))[..., None]) & (a > 0)
+    w = np.abs(oracle.dequant_nvfp4_ref(wr["codes"], wr["sf"], wr["g"])).reshape(-1, K // 16, 16)
+    ref["small"] = np.einsum("mb,mbi,nbi->mn", lsb, hit.astype(np.float64), w)
+    return ref
 
 
 def _check(lx, x, wq, wr, bias=None, out=None):
     K = x.shape[1]
     y = lx.lx_nvfp4_gemv(x, wq, None if bias is None else torch.from_numpy(bias).to(DEV), out=out)
     assert lx.lx_last_device_status() == 0
-    ref = oracle.gemv_nvfp4_ref(x.float().cpu().numpy(), wr, bias)
+    ref = _ref(x.float().cpu().numpy(), wr, bias)
     off = np.abs(y.float().cpu().numpy() - ref["y"])
     b = _bound(ref, K, bias)
     assert np.all(off <= b), f"{np.max(off / b):.3g} of the bound"
@@ -59,7 +75,7 @@ def test_shapes(lx, M, N, K):
 
 
 def test_long_k_in_several_segments(lx):
-    """K beyond what one CTA stages at a time (8 splits x 32 chunks of 128)."""
+    """Many turns of the ring in every CTA of a cluster, and an odd number of k-steps."""
     rng = np.random.default_rng(1)
     for M in (1, 16):
         K = 8 * 32 * 128 + 64 * 77
@@ -117,14 +133,10 @@ def test_wide_range_of_x(lx):
     x[7, 128:] = 0                                    # all-zero chunks
     xb = _bf16(x)
     y = lx.lx_nvfp4_gemv(xb, wq)
-    ref = oracle.gemv_nvfp4_ref(xb.float().cpu().numpy(), wr)
-    xf = np.abs(xb.float().cpu().numpy().astype(np.float64)).reshape(12, K // 128, 128)
-    # rounding of elements far below their chunk's largest: 2^-39 of it each
-    wmag = np.abs(nv.dequant_nvfp4_ref(wr["codes"], wr["sf"], wr["g"])).reshape(N, K // 128, 128).sum(-1)
-    small = 2.0 ** -39 * np.einsum("mc,nc->mn", xf.max(-1), wmag)
+    ref = _ref(xb.float().cpu().numpy(), wr)
     # results near the end of fp32's range: subnormal steps of the sums and of bf16
     off = np.abs(y.float().cpu().numpy() - ref["y"])
-    assert np.all(off <= _bound(ref, K) + small + 2.0 ** -133 + K * 2.0 ** -149)
+    assert np.all(off <= _bound(ref, K) + 2.0 ** -133 + K * 2.0 ** -149)
     assert torch.all(y[2] == 0)
 
 
@@ -133,7 +145,7 @@ def test_non_finite_x_stays_in_its_row(lx, bad):
     rng = np.random.default_rng(4)
     wq, wr = _weights(lx, rng, 150, 256)
     x = rng.standard_normal((3, 256))
-    clean = oracle.gemv_nvfp4_ref(_bf16(x).float().cpu().numpy(), wr)
+    clean = _ref(_bf16(x).float().cpu().numpy(), wr)
     x[1, 77] = bad
     y = lx.lx_nvfp4_gemv(_bf16(x), wq).float().cpu().numpy()
     for m in (0, 2):
@@ -163,7 +175,7 @@ def test_model_projections_sampled(lx):
         y = lx.lx_nvfp4_gemv(x, wq)
         rows = np.r_[0, 127, 128, N - 1, np.random.default_rng(N).choice(N, 60, replace=False)]
         wr = nv.quant_nvfp4_ref(W[torch.from_numpy(rows).to(DEV)].float().cpu().numpy(), wq.gscale.item())
-        ref = oracle.gemv_nvfp4_ref(x.float().cpu().numpy(), wr)
+        ref = _ref(x.float().cpu().numpy(), wr)
         assert np.all(np.abs(y.float().cpu().numpy()[:, rows] - ref["y"]) <= _bound(ref, K))
 
 
@@ -203,5 +215,5 @@ def test_capture_streams_and_repeatability(lx):
     x.copy_(_bf16(rng.standard_normal((3, 1024))))
     g.replay()
     torch.cuda.synchronize()
-    ref = oracle.gemv_nvfp4_ref(x.float().cpu().numpy(), wr)
+    ref = _ref(x.float().cpu().numpy(), wr)
     assert np.all(np.abs(out.float().cpu().numpy() - ref["y"]) <= _bound(ref, 1024))

@@ -499,7 +499,13 @@ def lx_nvfp4_gemm(xq: NvFp4Tensor, wq: NvFp4Tensor, bias=None, out=None, stream=
     return out
 
 
-def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, stream=None):
+def lx_nvfp4_gemv_ws_size(M, K) -> int:
+    b = ctypes.c_size_t()
+    _check(_abi.load().lx_nvfp4_gemv_ws_size(int(M), int(K), ctypes.byref(b)), "lx_nvfp4_gemv_ws_size")
+    return b.value
+
+
+def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None):
     """Y = x W^T + bias in bf16 [M, N] for M <= 16 bf16 rows x [M, K] and NVFP4 W [N, K]; bias fp32 [N] or None."""
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("expected a bf16 [M, K] tensor with contiguous rows")
@@ -512,10 +518,12 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, stream=None):
         raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != N):
         raise ValueError("bias must be a contiguous fp32 tensor of N elements")
+    if ws is None:
+        ws = torch.empty(lx_nvfp4_gemv_ws_size(M, wq.K), dtype=torch.uint8, device=x.device)
     ldx = x.stride(0) if M > 1 else max(x.stride(0), wq.K)
     ldy = out.stride(0) if M > 1 else max(out.stride(0), N)
     _check(_abi.load().lx_nvfp4_gemv(_ptr(x), M, ldx, _ptr(wq.codes), _ptr(wq.sf), _ptr(wq.gscale), _ptr(bias), N,
-                                     wq.K, _ptr(out), ldy, _stream(stream)), "lx_nvfp4_gemv")
+                                     wq.K, _ptr(out), ldy, _ptr(ws), ws.numel(), _stream(stream)), "lx_nvfp4_gemv")
     return out
 
 

@@ -485,46 +485,55 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   return Q->D == 128 ? run_packed<128>(t, p, two, s) : run_packed<64>(t, p, two, s);
 }
 // ---------------------------------------------------------------- NVFP4, few rows
-// CTAs per 128-row tile of the weights (a cluster along K).  Cost of a choice: the
-// CTAs of the fullest SM times the chunks of each; of equal ones the most CTAs, which
-// keep more loads in flight.
-int gemv_split(int64_t tiles, int64_t chunks, int sms) {
-  int best = 1;
-  int64_t cost = INT64_MAX;
-  for (int s = 1; s <= lx::kGvSplit && s <= chunks; ++s) {
-    const int64_t c = ((tiles * s + sms - 1) / sms) * ((chunks + s - 1) / s);
-    if (c <= cost) best = s, cost = c;
-  }
-  return best;
+// Workspace: the digit rows [8 M][K / 2], their scales, the rows' exponents.
+struct GemvWs {
+  size_t sf, ref, total;
+};
+GemvWs gemv_layout(int64_t M, int64_t K) {
+  GemvWs w;
+  w.sf = align256((size_t)(8 * M) * (size_t)(K / 2));
+  w.ref = w.sf + (size_t)(K / 64) * 512;
+  w.total = w.ref + 256;
+  return w;
 }
 
-template <int NT>
-lx_status launch_gemv(lx::GemvArgs a, int64_t tiles, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
+  const GemvWs w = gemv_layout(a.M, a.K);
+  uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
+  uint8_t* sf = codes + w.sf;
+  int* ref = reinterpret_cast<int*>(ws + w.ref);
+  a.xsf = sf;
+  a.ref = ref;
+  const int cols = lx::gemv_cols(a.M);
+  CUtensorMap tw, tx;
+  if (!make_map_codes(&tw, a.wc, a.N, a.K, 128) || !make_map_codes(&tx, codes, 8 * a.M, a.K, cols)) return LX_ERR_CUDA;
+  // as many CTAs per row tile as fit the GPU at once (two per SM), each with a stage at
+  // least: all loads are then in flight together, and few row tiles still fill it
+  const int64_t tiles = (a.N + 127) / 128, stages = ((int64_t)a.K + 255) / 256;
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>({lx::kGvSplit, lx::kPkSlots / tiles, stages}));
+  a.per = (int)((stages + split - 1) / split);
+  const int64_t slices = ((int64_t)a.K + lx::kGvSlice - 1) / lx::kGvSlice;
+  if (slices > 65535) return LX_ERR_UNSUPPORTED;
+  lx::nvfp4_gemv_digits_kernel<<<dim3((unsigned)a.M, (unsigned)slices), 128, 0, s>>>(a.x, a.ldx, a.K, codes, sf, ref);
+  if (cudaGetLastError() != cudaSuccess) return LX_ERR_CUDA;
+  const int smem = (int)lx::gemv_smem(cols);
+  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return LX_ERR_CUDA;
-  const int64_t chunks = ((int64_t)a.K + 127) / 128;
-  const int split = gemv_split(tiles, chunks, sms);
-  a.per = (int)((chunks + split - 1) / split);
-  if (tiles * split > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
-  using S = lx::GemvSmem<NT>;
-  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES) !=
-      cudaSuccess)
-    return LX_ERR_CUDA;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)split;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = S::BYTES;
+  cfg.blockDim = dim3(lx::kGvThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<NT>, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel, tw, tx, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
 }
 }  // namespace
 
@@ -1166,14 +1175,27 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
   return launch_status();
 }
 
+lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t K, size_t* bytes) {
+  if (!bytes || M < 1 || K < 64 || K % 64 != 0 || K > ((int64_t)1 << 24)) return LX_ERR_INVALID;
+  if (M > lx::kGvMaxRows) return LX_ERR_UNSUPPORTED;
+  *bytes = gemv_layout(M, K).total;
+  return LX_OK;
+}
+
 lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc, const uint8_t* wsf, const float* gw,
-                        const float* bias, int64_t N, int64_t K, void* y, int64_t ldy, cudaStream_t stream) {
+                        const float* bias, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, size_t ws_bytes,
+                        cudaStream_t stream) {
   if (!x || !wc || !wsf || !gw || !y) return LX_ERR_INVALID;
-  if (M < 1 || N < 1 || K < 64 || K % 64 != 0 || K > ((int64_t)1 << 30) || ldx < K || ldy < N) return LX_ERR_INVALID;
-  if (M > lx::kGvMaxRows || N > ((int64_t)1 << 31) - 256) return LX_ERR_UNSUPPORTED;
+  size_t need = 0;
+  lx_status st = lx_nvfp4_gemv_ws_size(M, K, &need);
+  if (st != LX_OK) return st;
+  if (N < 1 || ldx < K || ldy < N) return LX_ERR_INVALID;
+  if (N > ((int64_t)1 << 31) - 256) return LX_ERR_UNSUPPORTED;
   if (!al16(x) || ldx % 8 != 0 || !al16(wc) || !al16(wsf) || (reinterpret_cast<uintptr_t>(y) & 1u) ||
       ((reinterpret_cast<uintptr_t>(gw) | reinterpret_cast<uintptr_t>(bias)) & 3u))
     return LX_ERR_ALIGN;
+  if (!ws || ws_bytes < need) return LX_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
   lx::GemvArgs a{};
   a.x = reinterpret_cast<const __nv_bfloat16*>(x);
   a.wc = wc;
@@ -1186,8 +1208,8 @@ lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc
   a.N = N;
   a.M = (int)M;
   a.K = (int)K;
-  const int64_t tiles = (N + 127) / 128;
-  return M <= 8 ? launch_gemv<1>(a, tiles, stream) : launch_gemv<2>(a, tiles, stream);
+  a.limit_ns = kWaitLimitNs;
+  return launch_gemv(a, reinterpret_cast<char*>(ws), stream);
 }
 
 }  // extern "C"

@@ -393,13 +393,14 @@ lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t K, size_t* bytes);
 /* Y[m, n] = bf16(fl32(acc[m, n] * gw) + bias[n]) for M <= 16 bf16 rows x [M, K] (row
  * stride ldx elements, ldx % 8 == 0) that are not quantised: timestep modulation,
  * guided pairs, single new tokens.  acc = the fp32 sum over k of x[m, k] times the
- * weight's E2M1 value times its E4M3 block scale.  x enters exactly but for elements
- * below 2^-14 of the largest of their block of 16 (k / 16 alike), which are rounded by
- * at most 2^-22 of that largest one (2^-39 of the row's largest if that is more).
- * W = (wc, wsf, gw) [N, K] as written by lx_nvfp4_quantize, any N, K % 64 == 0 and at
- * most 2^24; bias fp32 [N] or NULL; y bf16 [M, N], row stride ldy >= N.  x, wc, wsf
- * 16-byte aligned; ws of the size above, 256-byte aligned, not shared by calls that
- * may overlap.  More rows are LX_ERR_UNSUPPORTED: lx_nvfp4_gemm is the form for them. */
+ * weight's E2M1 value times its E4M3 block scale.  x enters as fixed-point numbers
+ * below its row's largest finite magnitude: for M <= 8 elements down to 2^-35 of it
+ * are exact and the rounding of others is at most 2^-43 of it; for M > 8, 2^-14 and
+ * 2^-22.
+ * W = (wc, wsf, gw) [N, K] as written by lx_nvfp4_quantize, N at most 2^30, K % 64 == 0
+ * and at most 2^24; bias fp32 [N] or NULL; y bf16 [M, N], row stride ldy >= N.  x, wc, wsf
+ * 16-byte aligned; ws of the size above, 256-byte aligned, not shared by calls that may
+ * overlap.  More rows are LX_ERR_UNSUPPORTED: lx_nvfp4_gemm is the form for them. */
 lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc, const uint8_t* wsf, const float* gw,
                         const float* bias, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, size_t ws_bytes,
                         cudaStream_t stream);

@@ -97,7 +97,7 @@ def test_prefix_refusals(lib):
 
 def test_gemv_refusals(lib):
     x, c, f, g, y = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000
-    call = lambda x=x, M=1, ldx=256, c=c, f=f, g=g, b=None, N=100, K=256, y=y, ldy=100, ws=0x70000, wb=1 << 30: \
+    call = lambda x=x, M=1, ldx=256, c=c, f=f, g=g, b=None, N=100, K=256, y=y, ldy=100, ws=0x70000, wb=1 << 40: \
         lib.lx_nvfp4_gemv(x, M, ldx, c, f, g, b, N, K, y, ldy, ws, wb, S)
     for k in ("x", "c", "f", "g", "y"):
         assert call(**{k: None}) == INV
@@ -109,11 +109,11 @@ def test_gemv_refusals(lib):
     assert call(ldx=260) == ALI
     assert call(x=x + 2) == ALI and call(c=c + 8) == ALI and call(f=f + 8) == ALI
     assert call(g=g + 2) == ALI and call(b=0x60002) == ALI and call(y=y + 1) == ALI
+    assert call(K=(1 << 24) + 64, ldx=(1 << 24) + 64) == UNS
     n = ctypes.c_size_t()
-    assert lib.lx_nvfp4_gemv_ws_size(3, 320, ctypes.byref(n)) == 0
-    assert n.value == 3840 + 5 * 512 + 256             # 24 digit rows of 160 bytes, scales of 5 k-steps, exponents
+    size = lambda M, K: lib.lx_nvfp4_gemv_ws_size(M, K, ctypes.byref(n))
+    assert size(3, 320) == 0 and n.value == 3 * 16 * 160 + 256       # 16 digits for up to 8 rows
     assert call(M=3, K=320, ldx=320, wb=n.value - 1) == WSP and call(ws=None) == WSP and call(ws=0x70010) == ALI
-    assert lib.lx_nvfp4_gemv_ws_size(17, 320, ctypes.byref(n)) == UNS
-    assert lib.lx_nvfp4_gemv_ws_size(1, 100, ctypes.byref(n)) == INV
-    assert lib.lx_nvfp4_gemv_ws_size(1, (1 << 24) + 64, ctypes.byref(n)) == INV
-    assert lib.lx_nvfp4_gemv_ws_size(0, 64, ctypes.byref(n)) == INV and lib.lx_nvfp4_gemv_ws_size(1, 64, None) == INV
+    assert size(9, 320) == 0 and n.value == 9 * 8 * 160 + 256        # 11520 is a multiple of 256
+    assert size(17, 320) == UNS and size(1, (1 << 24) + 64) == UNS
+    assert size(1, 100) == INV and size(0, 64) == INV and lib.lx_nvfp4_gemv_ws_size(1, 64, None) == INV

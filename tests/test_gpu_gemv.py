@@ -5,10 +5,10 @@ Bound: |Y - y| <= 2^-8 |y| (bf16) + c 2^-23 (4 mag + |bias|) + r, mag = g sum_k 
 A digit column is an fp32 sum over MMA steps of 64 products; a step adds its products
 with at most 7 roundings (or truncations) of 2^-23 of what is summed and one into the
 column: 8 K / 64.  Eight columns (7 FMAs), 2 powers of two, 8 splits, the scale and
-the bias follow: c = K / 8 + 20.  The magnitudes of the digits of an element add up to
-less than 4 of its own (11 / 3 for a 1 above digits of -4).  r: elements of x
-below 2^-14 of their block's largest are rounded by 2^-22 of it (2^-39 of the row's
-largest if that is more), times the block's weights."""
+the bias follow (16 columns, 20 splits at most in these shapes): c = K / 8 + 50.  The magnitudes of the digits of an element add up to
+less than 4 of its own (11 / 3 for a 1 above digits of -4).  r: elements of x below
+2^-35 (up to 8 rows) or 2^-14 (more) of their row's largest are rounded by 2^-43 or
+2^-22 of it, times the weights they meet."""
 import numpy as np
 import pytest
 import torch
@@ -37,7 +37,7 @@ def _weights(lx, rng, N, K, scale=0.05):
 
 def _bound(ref, K, bias=None):
     mag = 4 * ref["mag"] + (0 if bias is None else np.abs(bias)[None, :])
-    return 2.0 ** -8 * np.abs(ref["y"]) + (K / 8 + 20) * 2.0 ** -23 * mag + ref["small"] + 1e-38
+    return 2.0 ** -8 * np.abs(ref["y"]) + (K / 8 + 50) * 2.0 ** -23 * mag + ref["small"] + 1e-38
 
 
 def _ref(x, wr, bias=None):
@@ -45,12 +45,12 @@ def _ref(x, wr, bias=None):
     x = np.asarray(x, np.float64)
     ref = oracle.gemv_nvfp4_ref(x, wr, bias)
     M, K = x.shape
-    a = np.abs(np.where(np.isfinite(x), x, 0)).reshape(M, K // 16, 16)
-    top = a.max(-1)
-    lsb = np.maximum(2.0 ** -22 * top, 2.0 ** -39 * top.max(-1, keepdims=True))
-    hit = (a < 2.0 ** -14 * np.maximum(top, 2.0 ** -17 * top.max(-1, keepdims=True))[..., None]) & (a > 0)
-    w = np.abs(oracle.dequant_nvfp4_ref(wr["codes"], wr["sf"], wr["g"])).reshape(-1, K // 16, 16)
-    ref["small"] = np.einsum("mb,mbi,nbi->mn", lsb, hit.astype(np.float64), w)
+    a = np.abs(np.where(np.isfinite(x), x, 0))
+    top = a.max(-1, keepdims=True)
+    exact, lsb = (-35, -43) if M <= 8 else (-14, -22)
+    hit = (a < 2.0 ** exact * top) & (a > 0)
+    w = np.abs(oracle.dequant_nvfp4_ref(wr["codes"], wr["sf"], wr["g"]))
+    ref["small"] = 2.0 ** lsb * top * (hit.astype(np.float64) @ w.T)
     return ref
 
 

@@ -485,55 +485,63 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   return Q->D == 128 ? run_packed<128>(t, p, two, s) : run_packed<64>(t, p, two, s);
 }
 // ---------------------------------------------------------------- NVFP4, few rows
-// Workspace: the digit rows [8 M][K / 2], their scales, the rows' exponents.
-struct GemvWs {
-  size_t sf, ref, total;
-};
-GemvWs gemv_layout(int64_t M, int64_t K) {
-  GemvWs w;
-  w.sf = align256((size_t)(8 * M) * (size_t)(K / 2));
-  w.ref = w.sf + (size_t)(K / 64) * 512;
-  w.total = w.ref + 256;
-  return w;
+// CTAs that share a 256-row tile of the weights (a cluster).  kFit[c]: clusters of c
+// such CTAs that a B200 holds at once (one CTA per SM; the GPCs' sizes decide).  Cost
+// of a choice: the waves times a CTA's stages, with about 6 stages' time for starting a
+// CTA and joining the sums.
+int gemv_split(int64_t tiles, int64_t stages) {
+  static const int kFit[lx::kGvSplit + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int c = 1; c <= lx::kGvSplit && c <= stages; ++c) {
+    const int64_t per = (stages + c - 1) / c;
+    if ((stages + per - 1) / per != c) continue;   // some CTA would have no stage
+    const int64_t t = ((tiles + kFit[c] - 1) / kFit[c]) * (per + 6);
+    if (t < cost) best = c, cost = t;
+  }
+  return best;
 }
 
+// Workspace: the digit rows [M P][K / 2], then the rows' exponents.
+inline int gemv_digits(int64_t M) { return M <= 8 ? 16 : 8; }
+inline size_t gemv_ref_offset(int64_t M, int64_t K) { return align256((size_t)(gemv_digits(M) * M) * (size_t)(K / 2)); }
+inline size_t gemv_ws_bytes(int64_t M, int64_t K) { return gemv_ref_offset(M, K) + 256; }
+
+template <int P>
 lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
-  const GemvWs w = gemv_layout(a.M, a.K);
   uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
-  uint8_t* sf = codes + w.sf;
-  int* ref = reinterpret_cast<int*>(ws + w.ref);
-  a.xsf = sf;
+  int* ref = reinterpret_cast<int*>(ws + gemv_ref_offset(a.M, a.K));
   a.ref = ref;
-  const int cols = lx::gemv_cols(a.M);
-  CUtensorMap tw, tx;
-  if (!make_map_codes(&tw, a.wc, a.N, a.K, 128) || !make_map_codes(&tx, codes, 8 * a.M, a.K, cols)) return LX_ERR_CUDA;
-  // as many CTAs per row tile as fit the GPU at once (two per SM), each with a stage at
-  // least: all loads are then in flight together, and few row tiles still fill it
-  const int64_t tiles = (a.N + 127) / 128, stages = ((int64_t)a.K + 255) / 256;
-  const int64_t split = std::max<int64_t>(1, std::min<int64_t>({lx::kGvSplit, lx::kPkSlots / tiles, stages}));
+  const int64_t tiles = (a.N + lx::kGvTile - 1) / lx::kGvTile, stages = ((int64_t)a.K + 255) / 256;
+  const int split = gemv_split(tiles, stages);
   a.per = (int)((stages + split - 1) / split);
-  const int64_t slices = ((int64_t)a.K + lx::kGvSlice - 1) / lx::kGvSlice;
-  if (slices > 65535) return LX_ERR_UNSUPPORTED;
-  lx::nvfp4_gemv_digits_kernel<<<dim3((unsigned)a.M, (unsigned)slices), 128, 0, s>>>(a.x, a.ldx, a.K, codes, sf, ref);
-  if (cudaGetLastError() != cudaSuccess) return LX_ERR_CUDA;
-  const int smem = (int)lx::gemv_smem(cols);
-  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  CUtensorMap tw, tx;
+  if (!make_map_codes(&tw, a.wc, a.N, a.K, lx::kGvTile) || !make_map_codes(&tx, codes, (int64_t)P * a.M, a.K, P * a.M))
     return LX_ERR_CUDA;
+  const int smem = (int)lx::GemvSmem<P>::bytes(a.M);
+  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return LX_ERR_CUDA;
+  // both kernels start while the work ahead of them ends (they wait for it themselves)
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)split;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.M, (unsigned)(((int64_t)a.K + lx::kGvSlice - 1) / lx::kGvSlice));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_digits_kernel<P>, a.x, a.ldx, a.K, codes, ref) != cudaSuccess)
+    return LX_ERR_CUDA;
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(lx::kGvThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel, tw, tx, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<P>, tw, tx, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
 }
 }  // namespace
 
@@ -1176,9 +1184,9 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
 }
 
 lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t K, size_t* bytes) {
-  if (!bytes || M < 1 || K < 64 || K % 64 != 0 || K > ((int64_t)1 << 24)) return LX_ERR_INVALID;
-  if (M > lx::kGvMaxRows) return LX_ERR_UNSUPPORTED;
-  *bytes = gemv_layout(M, K).total;
+  if (!bytes || M < 1 || K < 64 || K % 64 != 0) return LX_ERR_INVALID;
+  if (M > lx::kGvMaxRows || K > ((int64_t)1 << 24)) return LX_ERR_UNSUPPORTED;
+  *bytes = gemv_ws_bytes(M, K);
   return LX_OK;
 }
 
@@ -1190,7 +1198,7 @@ lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc
   lx_status st = lx_nvfp4_gemv_ws_size(M, K, &need);
   if (st != LX_OK) return st;
   if (N < 1 || ldx < K || ldy < N) return LX_ERR_INVALID;
-  if (N > ((int64_t)1 << 31) - 256) return LX_ERR_UNSUPPORTED;
+  if (N > ((int64_t)1 << 30)) return LX_ERR_UNSUPPORTED;
   if (!al16(x) || ldx % 8 != 0 || !al16(wc) || !al16(wsf) || (reinterpret_cast<uintptr_t>(y) & 1u) ||
       ((reinterpret_cast<uintptr_t>(gw) | reinterpret_cast<uintptr_t>(bias)) & 3u))
     return LX_ERR_ALIGN;
@@ -1209,7 +1217,8 @@ lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc
   a.M = (int)M;
   a.K = (int)K;
   a.limit_ns = kWaitLimitNs;
-  return launch_gemv(a, reinterpret_cast<char*>(ws), stream);
+  char* base = reinterpret_cast<char*>(ws);
+  return gemv_digits(M) == 16 ? launch_gemv<16>(a, base, stream) : launch_gemv<8>(a, base, stream);
 }
 
 }  // extern "C"

@@ -10,18 +10,20 @@
 // arrive (42 weights per clock; mma.sync on weights decoded to fp16 took 38 to 55 us
 // for 30720 x 5120, the format's conversion instruction or 5 instructions per weight
 // bounding it), so the block-scaled tensor core reads the codes as they are, and x
-// takes the weights' format: each row becomes 8 rows of signed octal digits.
+// takes the weights' format: each row becomes P rows of signed octal digits.
 //
-// Digits.  Within a block of 16 along k, whose largest finite magnitude lies in
-// [2^e, 2^(e+1)), x = X 2^(e-21) with an integer |X| <= 2^22 (x has 8 significant
-// bits: elements down to 2^-14 of the largest are exact, smaller ones are rounded by at
-// most 2^(e-22)).  X = sum_i d_i 8^i with d_i in {-4 .. 3}, read off the octal digits
-// of X + 44444444 (octal); every d_i is an E2M1 value, and the block's scale 2^(e - ref + 8)
-// an E4M3 one, ref the exponent of the row's largest element (blocks more than
-// 2^17 below it use the smallest scale; their rounding is 2^(ref-39)).  So
-//   acc = 2^(ref-29) sum_i 8^i D_i,  D_i = sum_k (w s) (d_i 2^(e-ref+8))
-// with D_i the fp32 sums of one MMA column each: 8 M columns.  Elements that are not
-// finite have zero digits; the rows that hold them add x w for those k in the epilogue.
+// Digits.  With 2^e the largest power of two in the finite magnitudes of a row of x,
+// x 2^(21-e) = H + L 2^-21 with integers
+// |H| <= 2^22 and |L| <= 2^20, both by rounding in fp32 (the remainder x 2^(21-e) - H is
+// exact).  Each is a sum of 8 octal digits in {-4 .. 3}, read off the octal digits of
+// H + 44444444 (octal); every digit is an E2M1 value.  So
+//   acc = 2^(e-21) (sum_i 8^i D_(P-8+i) + 2^-21 sum_i 8^i D_i)
+// with D the fp32 sums of one row of the MMA, which has 128: P = 16 rows (H and L) for
+// each of up to 8 rows of x, and P = 8 (H alone) for up to 16.  x has 8 significant
+// bits, so elements down to 2^-35 (2^-14) of the largest are exact and smaller ones are
+// rounded by at most 2^-43 (2^-22) of it.
+// Elements that are not finite have zero digits; the rows that hold them add x w for
+// those k at the end.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -32,28 +34,41 @@
 namespace lx {
 
 constexpr int kGvMaxRows = 16;                // rows of x
-constexpr int kGvSplit = 8;                   // most CTAs that share a row tile's K (a cluster)
+constexpr int kGvTile = 256;                  // weight rows of a CTA (columns of the MMA)
+constexpr int kGvSplit = 8;                   // most CTAs that share a tile's K (a cluster)
+constexpr uint32_t kGvBBytes = 256 * 128;     // stage: 256 weight rows x 256 codes
+constexpr uint32_t kGvSfBytes = 2 * 4 * 512;  // their scales
 constexpr int kGvSlice = 1024;                // elements of x per CTA of the digit pass
-constexpr uint32_t kGvABytes = 128 * 128;     // stage: 128 weight rows x 256 codes
-constexpr uint32_t kGvSfBytes = 4 * 512;      // their scales; as many for the digits
+constexpr int kGvThreads = 320;
+constexpr uint32_t kGvTmemCols = 512;   // sums 0 .. 255; ones 256 .. 259; scales 288 + 32 per stage
 
-// columns of the MMA (a multiple of 16) and what follows from them
-__host__ __device__ constexpr int gemv_cols(int M) { return (8 * M + 15) / 16 * 16; }
-__host__ __device__ constexpr uint32_t gemv_stage(int cols) { return kGvABytes + 2 * kGvSfBytes + 128u * (uint32_t)cols; }
-// two CTAs share an SM: 4 stages of 22 to 26 KB up to 48 columns, 3 of up to 36 KB beyond
-__host__ __device__ constexpr int gemv_stages(int cols) { return cols <= 48 ? 4 : 3; }
-__host__ __device__ constexpr uint32_t gemv_smem(int cols) { return 1024 + (uint32_t)gemv_stages(cols) * gemv_stage(cols); }
+// Stage: weights, scales, then one 128-byte row per digit row (a multiple of the
+// 8-row swizzle pattern).  The MMA reads 128 digit rows: what lies behind the M P that
+// are written is read too and not used, hence the slack behind the last stage.
+template <int P>
+struct GemvSmem {
+  __host__ __device__ static constexpr uint32_t x_bytes(int M) { return 128u * (uint32_t)(M * P); }
+  __host__ __device__ static constexpr uint32_t stage(int M) { return kGvBBytes + kGvSfBytes + x_bytes(M); }
+  __host__ __device__ static constexpr int stages(int M) { return stage(M) <= 40 * 1024 ? 5 : 4; }
+  __host__ __device__ static constexpr uint32_t bytes(int M) {
+    return 1024 + (uint32_t)stages(M) * stage(M) + 128 * 128 - x_bytes(M);
+  }
+};
+constexpr int kGvMaxStages = 5;
+static_assert(GemvSmem<16>::bytes(1) <= 227 * 1024 - 2048 && GemvSmem<16>::bytes(2) <= 227 * 1024 - 2048 &&
+                  GemvSmem<16>::bytes(8) <= 227 * 1024 - 2048 && GemvSmem<8>::bytes(16) <= 227 * 1024 - 2048,
+              "shared memory per CTA");
+static_assert(GemvSmem<16>::bytes(1) >= 1024 + (128 + kGvMaxRows) * 1024, "room for the sums");
 
-// ref of a row as the digit pass leaves it: biased exponent, bit 16 set when the row
-// holds an element that is not finite
+// ref of a row as the digit pass leaves it: biased exponent of the largest finite
+// magnitude, bit 16 set when the row holds an element that is not finite
 constexpr int kGvBadRow = 1 << 16;
 
 struct GemvArgs {
   const __nv_bfloat16* x;
+  const int* ref;       // [M]
   const uint8_t* wc;
   const uint8_t* wsf;
-  const uint8_t* xsf;   // scales of the digits, tiled like the weights'
-  const int* ref;       // [M]
   const float* gw;
   const float* bias;
   __nv_bfloat16* y;
@@ -62,119 +77,156 @@ struct GemvArgs {
   unsigned long long limit_ns;
 };
 
-__device__ __forceinline__ float pow2f(int e) {  // 2^e, -149 <= e <= 127
-  return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (e + 149));
+__device__ __forceinline__ float pow2f(int e) {  // 2^e, -126 <= e <= 127
+  return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// ---------------------------------------------------------------- digits of x
+// Eight octal digits (24 bits) as nibbles, then as bytes that hold the E2M1 codes of
+// digit - 4: two words, digits 0 .. 3 and 4 .. 7.
+__device__ __forceinline__ void octal_codes(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  x += (x & 0xFFF000u) * 15u;
+  x += (x & 0x0FC00FC0u) * 3u;
+  x += x & 0x38383838u;
+  lo = __byte_perm(0x0A0C0D0Eu, 0x05040200u, x);        // -4 -3 -2 -1 | 0 1 2 3
+  hi = __byte_perm(0x0A0C0D0Eu, 0x05040200u, x >> 16);
+}
+
+// Digit codes of 8 neighbouring elements: word[d] holds digit d of element i in nibble i.
+// f0 f1 = 2^(21-e) (in two factors: it may pass fp32's range).
+template <int P>
+__device__ __forceinline__ void gemv_digits8(const uint4& v, float f0, float f1, uint32_t (&word)[P]) {
+  constexpr float kMagic23 = 12582912.f;                 // 1.5 2^23: adding it leaves the rounded integer in the low bits
+  constexpr uint32_t kBias = 044444444u - 0x4B400000u;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t pr[P / 4][4];   // [group of 4 digits][pair of elements]: a byte per digit
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x = (h ? bf16hi(w[j]) : bf16lo(w[j])) * f0;
+      const float t = fmaf(x, f1, kMagic23);
+      uint32_t c[P / 4];
+      octal_codes(__float_as_uint(t) + kBias, c[P / 4 - 2], c[P / 4 - 1]);
+      if constexpr (P == 16) {
+        const float rest = fmaf(x, f1, -(t - kMagic23));  // exact
+        octal_codes(__float_as_uint(fmaf(rest, 2097152.f, kMagic23)) + kBias, c[0], c[1]);
+      }
+#pragma unroll
+      for (int q = 0; q < P / 4; ++q) pr[q][j] = h ? pr[q][j] + 16u * c[q] : c[q];
+    }
+#pragma unroll
+  for (int q = 0; q < P / 4; ++q) {
+    const uint32_t a = __byte_perm(pr[q][0], pr[q][1], 0x5140), b = __byte_perm(pr[q][2], pr[q][3], 0x5140);
+    const uint32_t c = __byte_perm(pr[q][0], pr[q][1], 0x7362), d = __byte_perm(pr[q][2], pr[q][3], 0x7362);
+    word[4 * q] = __byte_perm(a, b, 0x5410);
+    word[4 * q + 1] = __byte_perm(a, b, 0x7632);
+    word[4 * q + 2] = __byte_perm(c, d, 0x5410);
+    word[4 * q + 3] = __byte_perm(c, d, 0x7632);
+  }
+}
+
+// v with zeros in place of elements that are not finite
+__device__ __forceinline__ uint4 finite_only(uint4 v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+    if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // grid (M, ceil(K / kGvSlice)), 128 threads of 8 elements.  Every CTA reads the whole
-// row (it is short) for the row's largest element.
+// row (it is short) for its largest element.  codes: [M P][K / 2], row m P + d holds
+// digit d of x's row m.
+template <int P>
 __global__ void __launch_bounds__(128) nvfp4_gemv_digits_kernel(const __nv_bfloat16* __restrict__ x, long long ldx, int K,
-                                                                uint8_t* __restrict__ codes, uint8_t* __restrict__ sf,
-                                                                int* __restrict__ ref) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the weights may start to load
+                                                                uint8_t* __restrict__ codes, int* __restrict__ ref) {
+  // launched before the work ahead of it on the stream has ended; once that has, the
+  // product kernel may start to load the weights
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   const int m = blockIdx.x;
   const uint4* row = reinterpret_cast<const uint4*>(x + m * ldx);
+  const int k = blockIdx.y * kGvSlice + threadIdx.x * 8;
+  const uint4 mine = k < K ? row[k / 8] : make_uint4(0, 0, 0, 0);
   uint32_t top = 0, bad = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int v = threadIdx.x; v < K / 8; v += 128) {
-    const uint4 t = row[v];
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-      if (lo < 0x7F80u) top = max(top, lo); else bad = 1;
-      if (hi < 0x7F80u) top = max(top, hi); else bad = 1;
-    }
+    const uint4 t = row[v], f = finite_only(t);
+    bad |= (f.x ^ t.x) | (f.y ^ t.y) | (f.z ^ t.z) | (f.w ^ t.w);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(f.x & 0x7FFF7FFFu, f.y & 0x7FFF7FFFu),
+                                 __vmaxu2(f.z & 0x7FFF7FFFu, f.w & 0x7FFF7FFFu)));
   }
-  __shared__ uint32_t s_top, s_bad;
-  if (threadIdx.x == 0) s_top = 0, s_bad = 0;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, top);
+  __shared__ uint32_t s_top[4], s_bad[4];
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
   bad = __reduce_or_sync(0xffffffffu, bad);
   if ((threadIdx.x & 31) == 0) {
-    atomicMax(&s_top, top);
-    atomicOr(&s_bad, bad);
+    s_top[threadIdx.x >> 5] = top;
+    s_bad[threadIdx.x >> 5] = bad;
   }
   __syncthreads();
-  const int eref = max(1, (int)(s_top >> 7));
-  if (blockIdx.y == 0 && threadIdx.x == 0) ref[m] = eref | (s_bad ? kGvBadRow : 0);
-
-  const int k = blockIdx.y * kGvSlice + threadIdx.x * 8;
-  const bool live = k < K;
-  const uint4 t = live ? row[k / 8] : make_uint4(0, 0, 0, 0);
-  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-  uint32_t b[8];
-  uint32_t big = 0;
+  top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
+  bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+  const int biased = max(1, (int)(top >> 7)), e = 21 + 127 - biased;    // 2^e, in two factors
+  if (blockIdx.y == 0 && threadIdx.x == 0) ref[m] = biased | (bad ? kGvBadRow : 0);
+  if (k >= K) return;
+  uint32_t word[P];
+  gemv_digits8<P>(bad ? finite_only(mine) : mine, pow2f(e >> 1), pow2f(e - (e >> 1)), word);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    b[i] = (w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-    if ((b[i] & 0x7FFFu) >= 0x7F80u) b[i] = 0;
-    big = max(big, b[i] & 0x7FFFu);
-  }
-  big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));             // the block's other 8 elements
-  const int e = max(max(1, (int)(big >> 7)), eref - 17);
-  uint32_t word[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ex = (b[i] >> 7) & 0xFF, sh = 14 - (e - max(1, ex));
-    const int mant = (b[i] & 0x7F) | (ex ? 0x80 : 0);
-    int X = sh >= 0 ? mant << sh : (sh > -10 ? (mant + (1 << (-sh - 1))) >> -sh : 0);
-    X = (b[i] & 0x8000u) ? -X : X;
-    const uint32_t o = (uint32_t)(X + 044444444);
-#pragma unroll
-    for (int d = 0; d < 8; ++d)                                      // codes of -4 .. 3
-      word[d] |= ((0x5420ACDEu >> (((o >> (3 * d)) & 7u) * 4)) & 15u) << (4 * i);
-  }
-  if (!live) return;
-  const int se = 8 + e - eref;                                       // scale 2^se, -9 <= se <= 8
-  const uint8_t s8 = (uint8_t)(se >= -6 ? (se + 7) << 3 : 1 << (se + 9));
-#pragma unroll
-  for (int d = 0; d < 8; ++d) {
-    const int r = m * 8 + d;
-    *reinterpret_cast<uint32_t*>(codes + (long long)r * (K / 2) + k / 2) = word[d];
-    if ((threadIdx.x & 1) == 0) sf[(long long)(k / 64) * 512 + (r % 32) * 16 + (r / 32) * 4 + (k / 16) % 4] = s8;
-  }
+  for (int d = 0; d < P; ++d)
+    *reinterpret_cast<uint32_t*>(codes + (long long)(m * P + d) * (K / 2) + k / 2) = word[d];
 }
 
-// ---------------------------------------------------------------- products
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One CTA: 128 weight rows (the MMA's rows) against the digit columns over a range
-// of K; the CTAs of a cluster split K and add their sums over distributed shared
-// memory, in rank order.  Stages of 256 codes go through a ring: warp 0 loads
-// (the weights do not wait for the digit pass), warp 1 copies the scales into TMEM
-// and issues the MMAs, warps 2 .. 5 read the sums, thread = weight row.
-constexpr int kGvThreads = 192;
-constexpr uint32_t kGvTmemCols = 256;   // sums 0 .. 127; scales 128 + 32 per stage
-
-__global__ void __launch_bounds__(kGvThreads, 2) nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap tmW,
+// One CTA: the digit rows (the MMA's 128 rows) against 256 weight rows over a range of
+// K; one CTA per SM.  Stages of 256 codes go through a ring:
+//   warp 0: loads; those of the weights do not wait for the digit pass;
+//   warp 1: MMAs;
+//   warps 2 .. 5: move each stage's scales from shared memory to TMEM (a row of the
+//           tiled layout per lane, the same in all four lane quarters), then the
+//           sums.  tcgen05.cp does the same in the tensor pipe, where each copy of 512
+//           bytes took 70 clocks between MMAs of 128.
+// All ten warps then turn digit sums into outputs.  The digits' own scales are 1.  (Digits
+// made by warps of this kernel, stage by stage, were no faster for one row and cost
+// up to 40 us more for 16, every CTA reading its part of x twice.)  The CTAs of a cluster split K and add their sums over
+// distributed shared memory, in rank order.
+template <int P>
+__global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                    const __grid_constant__ CUtensorMap tmX,
                                                                    const GemvArgs a) {
+  using S = GemvSmem<P>;
   extern __shared__ uint8_t gv_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gv_smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bar_full[4], bar_empty[4], bar_acc, bar_drain;
+  // full/empty: a ring slot's loads; sf: its scales are in TMEM
+  __shared__ __align__(8) uint64_t bar_full[kGvMaxStages], bar_empty[kGvMaxStages], bar_sf[kGvMaxStages], bar_acc,
+      bar_drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int never_abort;
-  float* part = reinterpret_cast<float*>(sm);   // sums [row of x][128], in place of the stages once they are used
+  float* dsum = reinterpret_cast<float*>(sm);              // [digit row][256], in place of the stages once used
+  float* part = dsum + 128 * 256;                          // [row of x][256]
 
   uint32_t rank, ranks;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cols = gemv_cols(a.M), stages = gemv_stages(cols);
-  const uint32_t stage_bytes = gemv_stage(cols), b_bytes = 128u * (uint32_t)cols;
+  const int M = a.M, rows = M * P, stages = S::stages(M);
+  const uint32_t stage_bytes = S::stage(M);
   const int KS = a.K / 64, nkb = (KS + 3) / 4;
-  const int kb0 = min((int)rank * a.per, nkb), kb1 = min(kb0 + a.per, nkb), n = kb1 - kb0;
-  const int tile = (int)(blockIdx.x / ranks);
+  const int tile = blockIdx.x / ranks;
+  const int kb0 = rank * a.per, n = min(a.per, nkb - kb0);   // stages of this CTA (at least one)
+  const bool has1 = (long long)tile * 256 + 128 < a.N;       // the second scale tile exists
 
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
     for (int s = 0; s < stages; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], 1);
+      mbar_init(&bar_sf[s], 4);
     }
     mbar_init(&bar_acc, 1);
     mbar_init(&bar_drain, 1);
@@ -194,26 +246,23 @@ __global__ void __launch_bounds__(kGvThreads, 2) nvfp4_gemv_kernel(const __grid_
   if (warp == 0) {
     if (lane == 0) {
       // ================= loads =================
-      prefetch_tensormap(&tmW);
-      prefetch_tensormap(&tmX);
-      auto steps = [&](int kb) { return min(4, KS - 4 * kb); };      // k-steps of 64 in a stage
       auto load_w = [&](int i) {
         const int s = i % stages, kb = kb0 + i;
         uint8_t* st = sm + s * stage_bytes;
-        const uint32_t sfb = (uint32_t)steps(kb) * 512u;
-        mbar_arrive_expect_tx(&bar_full[s], kGvABytes + b_bytes + 2 * sfb);
-        tma_load_2d(st, &tmW, &bar_full[s], kb * 128, tile * 128);
-        bulk_load(st + kGvABytes, a.wsf + ((long long)tile * KS + kb * 4) * 512, sfb, &bar_full[s]);
+        const uint32_t sfb = (uint32_t)min(4, KS - 4 * kb) * 512u;     // k-steps of 64 in the stage
+        mbar_arrive_expect_tx(&bar_full[s], kGvBBytes + S::x_bytes(M) + (has1 ? 2u : 1u) * sfb);
+        tma_load_2d(st, &tmW, &bar_full[s], kb * 128, tile * 256);
+        bulk_load(st + kGvBBytes, a.wsf + ((long long)(2 * tile) * KS + kb * 4) * 512, sfb, &bar_full[s]);
+        if (has1)
+          bulk_load(st + kGvBBytes + 2048, a.wsf + ((long long)(2 * tile + 1) * KS + kb * 4) * 512, sfb, &bar_full[s]);
       };
       auto load_x = [&](int i) {
-        const int s = i % stages, kb = kb0 + i;
-        uint8_t* st = sm + s * stage_bytes + kGvABytes + kGvSfBytes;
-        bulk_load(st, a.xsf + (long long)kb * 4 * 512, (uint32_t)steps(kb) * 512u, &bar_full[s]);
-        tma_load_2d(st + kGvSfBytes, &tmX, &bar_full[s], kb * 128, 0);
+        const int s = i % stages;
+        tma_load_2d(sm + s * stage_bytes + kGvBBytes + kGvSfBytes, &tmX, &bar_full[s], (kb0 + i) * 128, 0);
       };
       const int first = min(n, stages);
       for (int i = 0; i < first; ++i) load_w(i);
-      asm volatile("griddepcontrol.wait;" ::: "memory");              // the digits are complete
+      asm volatile("griddepcontrol.wait;" ::: "memory");               // the digits are complete
       for (int i = 0; i < first; ++i) load_x(i);
       bool ok = true;
       int i = first;
@@ -234,27 +283,22 @@ __global__ void __launch_bounds__(kGvThreads, 2) nvfp4_gemv_kernel(const __grid_
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      // ================= scales -> TMEM, MMA =================
-      // block-scaled instruction: A, B = E2M1 (1), K-major, UE4M3 scales, 128 rows x cols
-      const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(cols >> 3) << 17) | (8u << 24);
+      // ================= MMA =================
       bool ok = true;
       for (int i = 0; i < n; ++i) {
         const int s = i % stages, steps = min(4, KS - 4 * (kb0 + i));
-        ok = mbar_wait(&bar_full[s], (uint32_t)(i / stages) & 1u, &abort_flag, a.limit_ns);
+        const uint32_t ph = (uint32_t)(i / stages) & 1u;
+        ok = mbar_wait(&bar_full[s], ph, &abort_flag, a.limit_ns) && mbar_wait(&bar_sf[s], ph, &abort_flag, a.limit_ns);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(sm + s * stage_bytes);
-        const uint32_t sfa = st + kGvABytes, sfb = sfa + kGvSfBytes, bt = sfb + kGvSfBytes;
-        for (int kk = 0; kk < steps; ++kk) {
-          const uint32_t ta = tb + 128u + (uint32_t)s * 32u + (uint32_t)kk * 4u, tx = ta + 16u;
-          tmem_cp_32x128b_x4(ta, smem_desc(sfa + kk * 512u, 128, 128, SW_NONE));
-          tmem_cp_32x128b_x4(tx, smem_desc(sfb + kk * 512u, 128, 128, SW_NONE));
-          mma_nvf4(tb, smem_desc(st + kk * 32u, 16, 1024, SW_128B), smem_desc(bt + kk * 32u, 16, 1024, SW_128B), idesc, ta,
-                   tx, (i | kk) != 0 ? 1u : 0u);
-        }
+        const uint32_t st = smem_u32(sm + s * stage_bytes), xt = st + kGvBBytes + kGvSfBytes;
+        const uint32_t tsf = tb + 288u + (uint32_t)s * 32u;
+        for (int kk = 0; kk < steps; ++kk)
+          mma_nvf4(tb, smem_desc(xt + kk * 32u, 16, 1024, SW_128B), smem_desc(st + kk * 32u, 16, 1024, SW_128B), kNvIdesc,
+                   tb + 256u, tsf + kk * 8u, (i | kk) != 0 ? 1u : 0u);
         mma_commit(&bar_empty[s]);
       }
-      if (ok && n > 0) mma_commit(&bar_acc);
+      if (ok) mma_commit(&bar_acc);
       if (!ok) {
         abort_flag = 1;
         report_error(-6);
@@ -264,78 +308,126 @@ __global__ void __launch_bounds__(kGvThreads, 2) nvfp4_gemv_kernel(const __grid_
       mbar_wait(&bar_drain, 0, &never_abort, a.limit_ns);
     }
     __syncwarp();
-  } else {
-    // ================= sums: 8 digit columns of a row -> one fp32 =================
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t taddr = tb + ((uint32_t)((warp & 3) * 32) << 16);
-    bool ok = n == 0 || warp_wait(&bar_acc, 0, &abort_flag, a.limit_ns);
+  } else if (warp < 6) {
+    // ================= scales to TMEM =================
+    const int quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    {
+      uint32_t one[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) one[i] = 0x38383838u;               // E4M3 1.0
+      tmem_st16(tb + lanes + 256u, one);
+    }
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % stages, steps = min(4, KS - 4 * (kb0 + i));
+      ok = warp_wait(&bar_full[s], (uint32_t)(i / stages) & 1u, &abort_flag, a.limit_ns);
+      if (!ok) break;
+      const uint4* sf = reinterpret_cast<const uint4*>(sm + s * stage_bytes + kGvBBytes) + lane;
+      uint32_t v[32];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 t = make_uint4(0, 0, 0, 0);
+          if (kk < steps && (h == 0 || has1)) t = sf[h * 128 + kk * 32];
+          v[kk * 8 + h * 4] = t.x;
+          v[kk * 8 + h * 4 + 1] = t.y;
+          v[kk * 8 + h * 4 + 2] = t.z;
+          v[kk * 8 + h * 4 + 3] = t.w;
+        }
+      tmem_st32(tb + lanes + 288u + (uint32_t)s * 32u, v);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_sf[s]);
+    }
+    // ================= sums: digit rows -> shared memory =================
+    if (ok) ok = warp_wait(&bar_acc, 0, &abort_flag, a.limit_ns);
     if (!ok) {
       abort_flag = 1;
       report_error(-6);
     }
     tc_fence_after();
-    const long long nr = (long long)tile * 128 + row;
-    for (int m0 = 0; m0 < a.M; m0 += 2) {
-      uint32_t d[16];
-      if (n > 0 && ok) {
-        tmem_ld16(taddr + 8 * m0, d);
+    if (ok && quarter * 32 < rows) {
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 64) {
+        uint32_t v[2][32];
+        tmem_ld32(tb + lanes + (uint32_t)c, v[0]);
+        tmem_ld32(tb + lanes + (uint32_t)c + 32u, v[1]);
         tmem_wait_ld();
+        reg_fence32(v[0]);
+        reg_fence32(v[1]);
+        // lane r writes row r: a turn of the 16-byte pieces keeps the banks apart
 #pragma unroll
-        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(d[i]));
-      }
+        for (int h = 0; h < 2; ++h) {
+          uint4* dst = reinterpret_cast<uint4*>(dsum + (quarter * 32 + lane) * 256 + c + 32 * h);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = m0 + h;
-        if (m >= a.M) break;
-        const int info = a.ref[m], e = (info & 0xFFFF) - 127;
-        float v = 0.f;
-        if (n > 0 && ok) {
-          v = __uint_as_float(d[8 * h + 7]);
-#pragma unroll
-          for (int i = 6; i >= 0; --i) v = fmaf(v, 8.f, __uint_as_float(d[8 * h + i]));
-          v = v * pow2f(e >> 1) * pow2f(e - (e >> 1) - 29);
+          for (int j = 0; j < 8; ++j)
+            dst[j ^ (lane & 7)] = make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
         }
-        if ((info & kGvBadRow) && nr < a.N) {
-          const long long end = min((long long)kb1 * 256, (long long)a.K);
-          for (long long k = (long long)kb0 * 256; k < end; ++k) {
-            const float xv = __bfloat162float(a.x[m * a.ldx + k]);
-            if (fabsf(xv) < INFINITY) continue;
-            const uint32_t c = (a.wc[nr * (a.K / 2) + k / 2] >> (4 * (k & 1))) & 15u, mag = c & 7u;
-            const uint32_t s8 = a.wsf[((long long)tile * KS + k / 64) * 512 + (row % 32) * 16 + (row / 32) * 4 + (k / 16) % 4];
-            float wv = mag < 4 ? 0.5f * mag : (mag < 6 ? (float)(mag - 2) : 2.f * (mag - 4));
-            wv *= e4m3_to_f32(s8);
-            v = fmaf(xv, (c & 8u) ? -wv : wv, v);
-          }
-        }
-        part[m * 128 + row] = v;
       }
     }
   }
+  // ================= one fp32 per output, by all warps =================
   tc_fence_before();
-  cluster_sync();
-  // every CTA of the cluster adds a share of the outputs, in rank order
-  const float gw = *a.gw;
-  const uint32_t base = smem_u32(part);
-  for (int i = (int)(rank * kGvThreads + threadIdx.x); i < 128 * a.M; i += (int)ranks * kGvThreads) {
-    const int m = i >> 7;
-    const long long nr = (long long)tile * 128 + (i & 127);
-    float s = 0.f;
-    for (uint32_t r = 0; r < ranks; ++r) {
-      uint32_t at;
-      float v;
-      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 4u * (uint32_t)i), "r"(r));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-      s += v;
-    }
-    if (nr < a.N) a.y[m * a.ldy + nr] = __float2bfloat16(__fadd_rn(__fmul_rn(s, gw), a.bias ? a.bias[nr] : 0.f));
-  }
-  // no CTA leaves while another may still read its sums
-  cluster_sync();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kGvTmemCols);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int o = threadIdx.x; o < M * 256; o += kGvThreads) {
+    const int m = o >> 8, col = o & 255, info = a.ref[m], e = (info & 0xFFFF) - 127;
+    float v = 0.f;
+#pragma unroll
+    for (int h = 0; h < P / 8; ++h) {   // the low digits first
+      float u = 0.f;
+#pragma unroll
+      for (int d = 7; d >= 0; --d) {
+        const int r = m * P + 8 * h + d;
+        u = fmaf(u, 8.f, dsum[r * 256 + (((col >> 2) ^ (r & 7)) << 2) + (col & 3)]);
+      }
+      v = fmaf(v, 0x1p-21f, u);
+    }
+    v = v * pow2f(e >> 1) * pow2f(e - (e >> 1) - 21);
+    const long long nr = (long long)tile * 256 + col;
+    if ((info & kGvBadRow) && nr < a.N) {
+      const int end = min((kb0 + n) * 256, a.K), row = col & 127;
+      const uint8_t* sf = a.wsf + (nr / 128) * KS * 512 + (row % 32) * 16 + (row / 32) * 4;
+      for (int k = kb0 * 256; k < end; ++k) {
+        const float xv = __bfloat162float(a.x[m * a.ldx + k]);
+        if (fabsf(xv) < INFINITY) continue;
+        const uint32_t c = (a.wc[nr * (a.K / 2) + k / 2] >> (4 * (k & 1))) & 15u, mag = c & 7u;
+        float wv = mag < 4 ? 0.5f * mag : (mag < 6 ? (float)(mag - 2) : 2.f * (mag - 4));
+        wv *= e4m3_to_f32(sf[(k / 64) * 512 + (k / 16) % 4]);
+        v = fmaf(xv, (c & 8u) ? -wv : wv, v);
+      }
+    }
+    part[o] = v;
+  }
+  // every CTA of the cluster adds a share of the outputs, in rank order
+  cluster_sync();
+  const float gw = *a.gw;
+  const uint32_t base = smem_u32(part);
+  for (int o = (int)(rank * kGvThreads + threadIdx.x); o < M * 256; o += (int)ranks * kGvThreads) {
+    const int m = o >> 8;
+    const long long nr = (long long)tile * 256 + (o & 255);
+    float v[kGvSplit];
+#pragma unroll
+    for (uint32_t r = 0; r < kGvSplit; ++r) {
+      uint32_t at;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 4u * (uint32_t)o), "r"(min(r, ranks - 1)));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(at) : "memory");
+    }
+    float s = v[0];
+#pragma unroll
+    for (uint32_t r = 1; r < kGvSplit; ++r)
+      if (r < ranks) s += v[r];
+    if (nr < a.N) a.y[m * a.ldy + nr] = __float2bfloat16(__fadd_rn(__fmul_rn(s, gw), a.bias ? a.bias[nr] : 0.f));
+  }
+  // no CTA leaves while another may still read its sums
+  cluster_sync();
 }
 
 }  // namespace lx

@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import math
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -379,27 +380,80 @@ def lx_sparse_attn(Q, K, V, keep, mode="int8fp8", plan: Plan | None = None, out=
 
 
 # ---------------------------------------------------------------- packed sequences
-def _pack(cu_q, cu_k, len_k):
-    n = cu_q.numel() - 1
-    for t, m in ((cu_q, n + 1), (cu_k, n + 1), (len_k, n)):
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != m or not t.is_contiguous()
-                              or not t.is_cuda):
-            raise ValueError("cu_q and cu_k: contiguous int32 CUDA tensors of n + 1 entries, len_k of n")
-    return _abi.LxPack(cu_q.data_ptr(), cu_k.data_ptr(), len_k.data_ptr() if len_k is not None else None, n)
+# These calls serve single tokens, where marshalling counts: sizes of workspaces are
+# kept per shape, and the stream is asked for by device.
+def _raw_stream(stream, device_index):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device_index)
 
 
-def _check_lse(lse, Q):
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (Q.shape[1], Q.shape[2])
-                            or not lse.is_contiguous()):
-        raise ValueError("lse: a contiguous fp32 [Hq, Tq] tensor")
+def _same_device(*tensors):
+    """The device index of CUDA tensors that are all on one device (None entries are skipped)."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors are on different devices")
+    if d < 0:
+        raise ValueError("expected CUDA tensors")
+    return d
+
+
+def _shape_only(H, L, D):
+    return LxBhld(4096, 1, H, L, D, 8, D, H * D)
+
+
+@lru_cache(maxsize=4096)
+def _packed_ws(Hq, Tq, Hkv, Tk, D, n) -> int:
+    b = ctypes.c_size_t()
+    q, k = _shape_only(Hq, Tq, D), _shape_only(Hkv, Tk, D)
+    _check(_abi.load().lx_attn_packed_ws_size(ctypes.byref(q), ctypes.byref(k), n, ctypes.byref(b)),
+           "lx_attn_packed_ws_size")
+    return b.value
+
+
+@lru_cache(maxsize=4096)
+def _prefix_ws(Hq, Tq, D) -> int:
+    b = ctypes.c_size_t()
+    q = _shape_only(Hq, Tq, D)
+    _check(_abi.load().lx_attn_prefix_ws_size(ctypes.byref(q), ctypes.byref(b)), "lx_attn_prefix_ws_size")
+    return b.value
 
 
 def lx_attn_packed_ws_size(Q, K, n) -> int:
-    b = ctypes.c_size_t()
-    q, k = bhld(Q), bhld(K)
-    _check(_abi.load().lx_attn_packed_ws_size(ctypes.byref(q), ctypes.byref(k), int(n), ctypes.byref(b)),
-           "lx_attn_packed_ws_size")
-    return b.value
+    return _packed_ws(Q.shape[1], Q.shape[2], K.shape[1], K.shape[2], Q.shape[3], int(n))
+
+
+def lx_attn_prefix_ws_size(Q) -> int:
+    return _prefix_ws(Q.shape[1], Q.shape[2], Q.shape[3])
+
+
+def _attn_packed(prefix, Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws, stream):
+    if out is None:
+        out = torch.empty_like(Q)
+    dev = _same_device(Q, K, V, out, cu_q, cu_k, len_k, lse, ws, *prefix)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _attn_packed(prefix, Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws, stream)
+    n = cu_q.numel() - 1
+    for t, m in ((cu_q, n + 1), (cu_k, n + 1), (len_k, n)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != m or not t.is_contiguous()):
+            raise ValueError("cu_q and cu_k: contiguous int32 tensors of n + 1 entries, len_k of n")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != Q.shape[1:3] or not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous fp32 [Hq, Tq] tensor")
+    q, k, v, o = bhld(Q), bhld(K), bhld(V), bhld(out)
+    if ws is None:
+        size = _prefix_ws(q.H, q.L, q.D) if prefix else _packed_ws(q.H, q.L, k.H, k.L, q.D, n)
+        ws = torch.empty(size, dtype=torch.uint8, device=Q.device) if size else None
+    ref = ctypes.byref
+    pk = _abi.LxPack(cu_q.data_ptr(), cu_k.data_ptr(), len_k.data_ptr() if len_k is not None else None, n)
+    tail = (ref(k), ref(v), ref(pk), 1 if causal else 0, q.D ** -0.5 if scale is None else scale, ref(o),
+            lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None,
+            ws.numel() * ws.element_size() if ws is not None else 0, _raw_stream(stream, dev))
+    if prefix:
+        kp, vp = bhld(prefix[0]), bhld(prefix[1])
+        _check(_abi.load().lx_attn_prefix(ref(q), ref(kp), ref(vp), *tail), "lx_attn_prefix")
+    else:
+        _check(_abi.load().lx_attn_packed(ref(q), *tail), "lx_attn_packed")
+    return out
 
 
 def lx_attn_packed(Q, K, V, cu_q, cu_k, causal=True, scale=None, len_k=None, out=None, lse=None, ws=None,
@@ -409,42 +463,13 @@ def lx_attn_packed(Q, K, V, cu_q, cu_k, causal=True, scale=None, len_k=None, out
     Q: bf16 [1, Hq, Tq, D]; K, V: [1, Hkv, Tk, D]; cu_q, cu_k: int32 [n + 1] starts and ends; len_k: int32 [n]
     keys in use (caches).  scale None: 1 / sqrt(D).  lse: fp32 [Hq, Tq] to be filled, or None.  Rows outside
     [cu_q[0], cu_q[n]) of `out` and `lse` are left as they were.  Returns out."""
-    if out is None:
-        out = torch.empty_like(Q)
-    pk = _pack(cu_q, cu_k, len_k)
-    _check_lse(lse, Q)
-    if ws is None:
-        ws = torch.empty(max(lx_attn_packed_ws_size(Q, K, pk.n), 256), dtype=torch.uint8, device=Q.device)
-    q, k, v, o = bhld(Q), bhld(K), bhld(V), bhld(out)
-    scale = Q.shape[-1] ** -0.5 if scale is None else float(scale)
-    _check(_abi.load().lx_attn_packed(ctypes.byref(q), ctypes.byref(k), ctypes.byref(v), ctypes.byref(pk), int(causal),
-                                      scale, ctypes.byref(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
-           "lx_attn_packed")
-    return out
-
-
-def lx_attn_prefix_ws_size(Q) -> int:
-    b = ctypes.c_size_t()
-    q = bhld(Q)
-    _check(_abi.load().lx_attn_prefix_ws_size(ctypes.byref(q), ctypes.byref(b)), "lx_attn_prefix_ws_size")
-    return b.value
+    return _attn_packed((), Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws, stream)
 
 
 def lx_attn_prefix(Q, Kp, Vp, K, V, cu_q, cu_k, causal=True, scale=None, len_k=None, out=None, lse=None, ws=None,
                    stream=None):
     """lx_attn_packed for a batch whose rows all see the keys Kp, Vp [1, Hkv, Lp, D] before their own."""
-    if out is None:
-        out = torch.empty_like(Q)
-    pk = _pack(cu_q, cu_k, len_k)
-    _check_lse(lse, Q)
-    if ws is None:
-        ws = torch.empty(lx_attn_prefix_ws_size(Q), dtype=torch.uint8, device=Q.device)
-    q, kp, vp, k, v, o = bhld(Q), bhld(Kp), bhld(Vp), bhld(K), bhld(V), bhld(out)
-    scale = Q.shape[-1] ** -0.5 if scale is None else float(scale)
-    _check(_abi.load().lx_attn_prefix(ctypes.byref(q), ctypes.byref(kp), ctypes.byref(vp), ctypes.byref(k),
-                                      ctypes.byref(v), ctypes.byref(pk), int(causal), scale, ctypes.byref(o),
-                                      _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "lx_attn_prefix")
-    return out
+    return _attn_packed((Kp, Vp), Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws, stream)
 
 
 # ---------------------------------------------------------------- NVFP4
@@ -499,6 +524,7 @@ def lx_nvfp4_gemm(xq: NvFp4Tensor, wq: NvFp4Tensor, bias=None, out=None, stream=
     return out
 
 
+@lru_cache(maxsize=4096)
 def lx_nvfp4_gemv_ws_size(M, K) -> int:
     b = ctypes.c_size_t()
     _check(_abi.load().lx_nvfp4_gemv_ws_size(int(M), int(K), ctypes.byref(b)), "lx_nvfp4_gemv_ws_size")
@@ -509,21 +535,28 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
     """Y = x W^T + bias in bf16 [M, N] for M <= 16 bf16 rows x [M, K] and NVFP4 W [N, K]; bias fp32 [N] or None."""
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("expected a bf16 [M, K] tensor with contiguous rows")
-    if x.shape[1] != wq.K:
+    M, K = x.shape
+    N = wq.R
+    if K != wq.K:
         raise ValueError("x and W differ in K")
-    M, N = x.shape[0], wq.R
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1:
+    elif out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
         raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != N):
         raise ValueError("bias must be a contiguous fp32 tensor of N elements")
+    dev = _same_device(x, out, wq.codes, wq.sf, wq.gscale, bias, ws)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return lx_nvfp4_gemv(x, wq, bias, out, ws, stream)
     if ws is None:
-        ws = torch.empty(lx_nvfp4_gemv_ws_size(M, wq.K), dtype=torch.uint8, device=x.device)
-    ldx = x.stride(0) if M > 1 else max(x.stride(0), wq.K)
+        ws = torch.empty(lx_nvfp4_gemv_ws_size(M, K), dtype=torch.uint8, device=x.device)
+    ldx = x.stride(0) if M > 1 else max(x.stride(0), K)
     ldy = out.stride(0) if M > 1 else max(out.stride(0), N)
-    _check(_abi.load().lx_nvfp4_gemv(_ptr(x), M, ldx, _ptr(wq.codes), _ptr(wq.sf), _ptr(wq.gscale), _ptr(bias), N,
-                                     wq.K, _ptr(out), ldy, _ptr(ws), ws.numel(), _stream(stream)), "lx_nvfp4_gemv")
+    _check(_abi.load().lx_nvfp4_gemv(x.data_ptr(), M, ldx, wq.codes.data_ptr(), wq.sf.data_ptr(), wq.gscale.data_ptr(),
+                                     bias.data_ptr() if bias is not None else None, N, K, out.data_ptr(), ldy,
+                                     ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev)),
+           "lx_nvfp4_gemv")
     return out
 
 

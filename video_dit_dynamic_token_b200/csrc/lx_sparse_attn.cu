@@ -377,13 +377,19 @@ bool pack_two_tiles(int64_t Tq, int64_t n, int64_t G, int64_t Hkv) {
 }
 
 // Room for partial rows: as many splits as 64 MB hold, 2 to 128 (behind a prefix
-// one of its own and one of the sequence's are the least).
+// one of its own and one of the sequence's are the least); none where every
+// sequence is one split.
 struct PackWs {
   int64_t splits;
   size_t ml, part, total;   // [chunk | ml | part]
 };
-PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D) {
-  PackWs w;
+PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D, int64_t Tk, bool prefix) {
+  PackWs w{};
+  // no sequence is longer than the shortest split: nothing to join
+  if (!prefix && Tk <= lx::kPkSplitKeys * lx::kPkKeys) {
+    w.splits = 1;
+    return w;
+  }
   const int64_t R = Tq * Hq, row = 4 * D + 8;
   w.splits = std::max<int64_t>(2, std::min<int64_t>(128, ((int64_t)64 << 20) / (R * row)));
   w.ml = 256;
@@ -424,7 +430,7 @@ lx_status run_packed(const CUtensorMap* t, lx::PackParams p, bool two, cudaStrea
   const int64_t blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
   if (items > 0x7FFFFFFF || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
   lx_status st = launch_packed<D, 1>(t, p, dim3((unsigned)items), s);
-  if (st != LX_OK) return st;
+  if (st != LX_OK || !p.part) return st;
   lx::packed_combine_kernel<D><<<(unsigned)blocks, 256, 0, s>>>(p);
   return launch_status();
 }
@@ -445,13 +451,15 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   const bool two = !Kp && pack_two_tiles(Q->L, pack->n, G, K->H);
   lx::PackParams p{};
   if (!two) {
-    const PackWs w = pack_layout(Q->L, Q->H, Q->D);
-    if (!ws || ws_bytes < w.total) return LX_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
-    char* base = reinterpret_cast<char*>(ws);
-    p.chunk = reinterpret_cast<int*>(base);
-    p.ml = reinterpret_cast<float2*>(base + w.ml);
-    p.part = reinterpret_cast<float*>(base + w.part);
+    const PackWs w = pack_layout(Q->L, Q->H, Q->D, K->L, Kp != nullptr);
+    if (w.total) {
+      if (!ws || ws_bytes < w.total) return LX_ERR_WORKSPACE;
+      if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
+      char* base = reinterpret_cast<char*>(ws);
+      p.chunk = reinterpret_cast<int*>(base);
+      p.ml = reinterpret_cast<float2*>(base + w.ml);
+      p.part = reinterpret_cast<float*>(base + w.part);
+    }
     p.max_np = Kp ? (int)(w.splits / 2) : 0;
     p.max_ns = (int)(w.splits - p.max_np);
   }
@@ -476,9 +484,9 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   p.lse = lse;
   p.limit_ns = kWaitLimitNs;
   CUtensorMap t[5];
-  const lx_bhld* kv[4] = {K, V, Kp ? Kp : K, Kp ? Vp : V};
+  const lx_bhld* kv[4] = {K, V, Kp, Vp};
   if (!make_map_grouped(&t[0], Q, K->H, p.TQ)) return LX_ERR_CUDA;
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < (Kp ? 4 : 2); ++i)
     if (!make_map(&t[1 + i], kv[i]->data, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 1, kv[i]->H, kv[i]->L, kv[i]->D,
                   kv[i]->sB, kv[i]->sH, kv[i]->sL, 64, lx::kPkKeys))
       return LX_ERR_CUDA;
@@ -979,7 +987,7 @@ lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, 
   lx_status st;
   if ((st = check_packed(Q, K, K, Q)) != LX_OK) return st;
   if (!bytes || n < 1) return LX_ERR_INVALID;
-  *bytes = pack_two_tiles(Q->L, n, Q->H / K->H, K->H) ? 0 : pack_layout(Q->L, Q->H, Q->D).total;
+  *bytes = pack_two_tiles(Q->L, n, Q->H / K->H, K->H) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, false).total;
   return LX_OK;
 }
 
@@ -992,7 +1000,7 @@ lx_status lx_attn_prefix_ws_size(const lx_bhld* Q, size_t* bytes) {
   lx_status st = check_bhld(Q);
   if (st != LX_OK) return st;
   if (!bytes || Q->B != 1) return LX_ERR_INVALID;
-  *bytes = pack_layout(Q->L, Q->H, Q->D).total;
+  *bytes = pack_layout(Q->L, Q->H, Q->D, 0, true).total;
   return LX_OK;
 }
 

@@ -237,7 +237,7 @@ __device__ bool pack_find(const PackParams& p, PackItem* shared_item, int* warp_
     int c = (int)((n_work + share - 1) / share);
     c = max(max(c, kPkSplitKeys), pack_div(longest, p.max_ns));
     if (p.Lp) c = max(c, pack_div(pt, p.max_np));
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.chunk = c;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.chunk) *p.chunk = c;
     const int np = p.Lp ? pack_splits(pt, c, p.max_np) : 0;
     const int head = blockIdx.x % p.Hkv;
     int x = blockIdx.x / p.Hkv;

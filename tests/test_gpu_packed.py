@@ -135,10 +135,9 @@ def test_large_scores_rescale_the_accumulator(lx):
 
 @pytest.mark.parametrize("hq,hkv,D", [(40, 40, 128), (40, 8, 128), (32, 8, 64)])
 def test_prompts_that_fill_the_gpu(lx, hq, hkv, D):
-    """Enough rows for the two-tile form; checked on sampled heads and rows."""
+    """Several items for every SM; checked on sampled heads."""
     lq = [700, 33, 1500, 257]
     Q, K, V, out, lse = _run(lx, lq, lq, hq, hkv, D, True, seed=10, spare=5, ref=False)
-    assert lx.lx_attn_packed_ws_size(Q, K, 4) == 0
     cu = _cu(lq)
     for h in (0, hq // 2 + 1, hq - 1):
         g = h // (hq // hkv)
@@ -146,14 +145,14 @@ def test_prompts_that_fill_the_gpu(lx, hq, hkv, D):
         _check(out[:, h:h + 1], lse[h:h + 1], r, D)
 
 
-def test_two_tile_form_equals_one_tile_form(lx):
-    """The same sequences alone (one row tile, keys split) and in a large pack."""
-    D, hq, hkv = 128, 8, 8
-    lq = [400, 900, 130] * 8
+def test_alone_and_in_a_large_pack(lx):
+    """The same sequences by themselves (keys split over the SMs) and in a pack that needs no split."""
+    D, hq, hkv = 128, 40, 40
+    lq = [400, 900, 130] * 4
     Q, K, V, out, lse = _run(lx, lq, lq, hq, hkv, D, True, seed=11, ref=False)
     assert lx.lx_attn_packed_ws_size(Q, K, len(lq)) == 0
     cu = _cu(lq)
-    for i in (0, 1, 2, 23):
+    for i in (0, 1, 2, 11):
         a, b = cu[i], cu[i + 1]
         l1 = torch.empty((hq, b - a), device=DEV)
         o1 = lx.lx_attn_packed(Q[:, :, a:b], K[:, :, a:b], V[:, :, a:b], _i32([0, b - a]), _i32([0, b - a]), lse=l1)

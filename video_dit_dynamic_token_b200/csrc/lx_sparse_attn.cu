@@ -368,12 +368,11 @@ bool make_map_grouped(CUtensorMap* m, const lx_bhld* t, int64_t Hkv, int tokens)
 
 inline int pack_tokens(int64_t G) { return (int)(128 / G); }
 
-// Prompts run two row tiles per CTA, when there are enough such items for one
-// on every SM and a sequence fills more than one row tile on average; other
-// calls run one row tile per CTA with the keys split.
-bool pack_two_tiles(int64_t Tq, int64_t n, int64_t G, int64_t Hkv) {
+// Prompts that give every SM several items, more than a row tile of each sequence on
+// average, gain nothing from splitting keys: such calls need no workspace.
+bool pack_fills(int64_t Tq, int64_t n, int64_t G, int64_t Hkv) {
   const int64_t TQ = pack_tokens(G);
-  return Hkv * (Tq / (2 * TQ)) >= lx::kPkSlots / 2 && Tq > n * TQ;
+  return Hkv * (Tq / (2 * TQ)) >= 3 * lx::kPkSMs && Tq > n * TQ;
 }
 
 // Room for partial rows: as many splits as 64 MB hold, 2 to 128 (behind a prefix
@@ -409,27 +408,20 @@ lx_status check_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, con
   return LX_OK;
 }
 
-template <int D, int NQ>
-lx_status launch_packed(const CUtensorMap* t, const lx::PackParams& p, dim3 grid, cudaStream_t s) {
-  using C = lx::PackCfg<D, NQ>;
-  if (cudaFuncSetAttribute(lx::packed_attn_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+template <int D>
+lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t s) {
+  using C = lx::PackCfg<D>;
+  // upper bounds: the lengths are on the device.  Splits add less than a round for every
+  // SM three times over (items of at least a third of a CTA's share of the work).
+  const int64_t rows = 2 * p.TQ, tiles = p.Tq / rows + std::min(p.n, p.Tq);
+  const int64_t prefix = p.Lp ? p.Tq / rows + 1 : 0, splits = p.part ? 3 * (lx::kPkSMs + p.Hkv) : 0;
+  const int64_t items = splits + (tiles + prefix) * p.Hkv, blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
+  if (items > 0x7FFFFFFE || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(lx::packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
     return LX_ERR_CUDA;
-  lx::packed_attn_kernel<D, NQ><<<grid, C::THREADS, C::SMEM, s>>>(t[0], t[1], t[2], t[3], t[4], p);
-  return launch_status();
-}
-
-template <int D>
-lx_status run_packed(const CUtensorMap* t, lx::PackParams p, bool two, cudaStream_t s) {
-  // upper bounds: the lengths are on the device
-  const int64_t rows = two ? 2 * p.TQ : p.TQ;
-  const int64_t tiles = p.Tq / rows + std::min(p.n, p.Tq);
-  if (two) return launch_packed<D, 2>(t, p, dim3((unsigned)tiles, (unsigned)p.Hkv), s);
-  const int64_t prefix = p.Lp ? (p.Tq + rows - 1) / rows : 0;
-  const int64_t items = lx::kPkSlots + (tiles + prefix + 1) * p.Hkv;
-  const int64_t blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
-  if (items > 0x7FFFFFFF || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
-  lx_status st = launch_packed<D, 1>(t, p, dim3((unsigned)items), s);
+  lx::packed_attn_kernel<D><<<(unsigned)items, C::THREADS, C::SMEM, s>>>(t[0], t[1], t[2], t[3], t[4], p);
+  lx_status st = launch_status();
   if (st != LX_OK || !p.part) return st;
   lx::packed_combine_kernel<D><<<(unsigned)blocks, 256, 0, s>>>(p);
   return launch_status();
@@ -448,9 +440,9 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
        reinterpret_cast<uintptr_t>(pack->len_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
     return LX_ERR_ALIGN;
   const int64_t G = Q->H / K->H;
-  const bool two = !Kp && pack_two_tiles(Q->L, pack->n, G, K->H);
   lx::PackParams p{};
-  if (!two) {
+  p.max_ns = 1;
+  if (Kp || !pack_fills(Q->L, pack->n, G, K->H)) {
     const PackWs w = pack_layout(Q->L, Q->H, Q->D, K->L, Kp != nullptr);
     if (w.total) {
       if (!ws || ws_bytes < w.total) return LX_ERR_WORKSPACE;
@@ -490,7 +482,7 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
     if (!make_map(&t[1 + i], kv[i]->data, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 1, kv[i]->H, kv[i]->L, kv[i]->D,
                   kv[i]->sB, kv[i]->sH, kv[i]->sL, 64, lx::kPkKeys))
       return LX_ERR_CUDA;
-  return Q->D == 128 ? run_packed<128>(t, p, two, s) : run_packed<64>(t, p, two, s);
+  return Q->D == 128 ? run_packed<128>(t, p, s) : run_packed<64>(t, p, s);
 }
 // ---------------------------------------------------------------- NVFP4, few rows
 // CTAs that share a 256-row tile of the weights (a cluster).  kFit[c]: clusters of c
@@ -987,7 +979,7 @@ lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, 
   lx_status st;
   if ((st = check_packed(Q, K, K, Q)) != LX_OK) return st;
   if (!bytes || n < 1) return LX_ERR_INVALID;
-  *bytes = pack_two_tiles(Q->L, n, Q->H / K->H, K->H) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, false).total;
+  *bytes = pack_fills(Q->L, n, Q->H / K->H, K->H) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, false).total;
   return LX_OK;
 }
 

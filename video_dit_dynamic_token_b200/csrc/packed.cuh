@@ -12,22 +12,27 @@
 // tokens a tile, so that grouped heads read K and V once and a single token
 // still fills G rows.
 //
-// A work item is one CTA: NQ row tiles of one sequence (or of all tokens, for
-// the prefix) against a range of 128-key tiles of one key/value head.
-//   NQ = 2: prompts.  Two row tiles share each K/V tile; while one tile's
-//           softmax runs, the tensor core works for the other.  One CTA per SM.
-//   NQ = 1: few rows.  One row tile, two CTAs per SM, and the key range cut
-//           into splits when there are fewer items than CTA slots; each split
-//           leaves its unnormalised fp32 rows and (max, sum), and
-//           packed_combine_kernel joins them.
+// A work item keeps two streams of a CTA busy, each with a row tile of Q, its
+// softmax warpgroup and its accumulator in TMEM; while one stream's softmax runs, the
+// tensor core works for the other.  A sequence of more than TQ tokens gives each stream a
+// row tile of its own and both the same 128-key tiles (loaded once); a shorter one, such
+// as a single token, gives both the same rows and each a range of keys of its own.
+// Key ranges (splits) also spread long sequences over the SMs when there are few items:
+// a split leaves its unnormalised fp32 rows and (max, sum), and packed_combine_kernel
+// joins them.  A row whose keys are one split is finished by its item.
 //
-// Roles: warps 0 .. 4 NQ - 1 softmax (thread = row; warpgroup g owns row tile
-// g), then one TMA warp and one MMA warp.  TMEM: S_g (128 fp32 columns, reused
-// for P as 64 columns of bf16 pairs) and O_g (D fp32 columns).  The MMA warp's
-// order per key tile j is PV_g(j), S_g(j+1) for each g: S_g(j+1) may overwrite
-// the columns of P_g(j) because the tensor core runs a CTA's MMAs in order, and
-// the commit of S_g(j+1) also says that PV_g(j) is complete, so the softmax
-// may rescale O_g without another barrier.
+// One CTA per SM.  The grid has a block for every item there can be; a running CTA takes
+// over blocks that have not started (cluster launch control), so that items are
+// handed out as CTAs become free, and the loads and first scores of an item run under the
+// end of the one before it.
+//
+// Roles: warps 0 .. 7 softmax (thread = row; warpgroup g is stream g); in the last
+// warpgroup one warp that takes items and loads, and one for the MMAs; each walks the
+// items by itself.  TMEM: S_g (128 fp32 columns, reused for P as 64 columns of bf16
+// pairs) and O_g (D fp32 columns).  The MMA warp's order per key tile j is PV_g(j),
+// S_g(j+1) for each g: S_g(j+1) may overwrite the columns of P_g(j) because the tensor
+// core runs a CTA's MMAs in order, and the commit of S_g(j+1) also says that PV_g(j)
+// is complete, so the softmax may rescale O_g without another barrier.
 //
 // The running maximum moves only when it grows by more than 2^8 (a shift that
 // leaves the quotient unchanged: P stays below 256 and its bf16 rounding is
@@ -51,23 +56,26 @@ namespace lx {
 
 constexpr int kPkKeys = 128;         // keys of a tile
 constexpr int kPkSplitKeys = 2;      // a split covers at least this many tiles
-constexpr int kPkSlots = 2 * 148;    // CTA slots of a B200 at two CTAs per SM
+constexpr int kPkFine = 6;           // from this many tiles on, three splits for a CTA's share of the work
+constexpr int kPkSMs = 148;
+constexpr int kPkItems = 4;          // items published ahead of their last reader
 constexpr float kPkLazy = 8.0f;      // log2 growth of the row maximum that forces a rescale
 
-template <int D, int NQ>
+template <int D>
 struct PackCfg {
   static constexpr int NATOM = D / 64;                 // 128-byte swizzle atoms per row
   static constexpr int TILE_BYTES = 128 * D * 2;       // a Q, K or V tile
-  // ring of K and V tiles: 5 x 32 KB beside 64 KB of Q (NQ = 2); 2 x 32 KB beside
-  // 32 KB of Q in half an SM (NQ = 1); twice as many for D = 64
-  static constexpr int RING = NQ == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 4);
-  static constexpr int OFF_RING = NQ * TILE_BYTES;
+  static constexpr int RING = D == 128 ? 5 : 8;        // K and V tiles beside the two of Q
+  static constexpr int OFF_RING = 2 * TILE_BYTES;
   static constexpr int SMEM = 1024 + OFF_RING + RING * TILE_BYTES;
-  static constexpr int WARPS = 4 * NQ + 2;
-  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int READERS = 9;                    // warps that read an item: softmax, MMA
+  static constexpr int THREADS = 384;                  // softmax warpgroups; loads, MMA and two idle warps
+  // registers per thread: 168 at launch, then moved to the softmax, whose threads hold a
+  // row of 128 scores: 128 x 72 + 256 x 216 = 384 x 168
+  static constexpr int REGS_AUX = 72, REGS_SOFTMAX = 216;
   static constexpr uint32_t S_COL = 0;                 // + 128 g
-  static constexpr uint32_t O_COL = 128 * NQ;          // + D g
-  static constexpr uint32_t TMEM_COLS = 256 * NQ;
+  static constexpr uint32_t O_COL = 256;               // + D g
+  static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t IDESC_S = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 0, 128, kPkKeys);
   static constexpr uint32_t IDESC_PV = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 1, 128, D);
 };
@@ -83,9 +91,9 @@ struct PackParams {
   __nv_bfloat16* o;
   long long osH, osL;
   float* lse;            // [Hq][Tq] or null
-  float* part;           // NQ = 1: [max_np + max_ns][Tq * Hq][D] unnormalised rows
-  float2* ml;            // NQ = 1: [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
-  int* chunk;            // NQ = 1: tiles per split, for the combine kernel
+  float* part;           // [max_np + max_ns][Tq * Hq][D] unnormalised rows; null where nothing is split
+  float2* ml;            // [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
+  int* chunk;            // tiles per split, for the combine kernel
   int max_np, max_ns;    // most splits of the prefix, of a sequence
   unsigned long long limit_ns;
 };
@@ -124,176 +132,212 @@ __device__ __forceinline__ PackSeq pack_all(const PackParams& p) {
 
 __device__ __forceinline__ int pack_div(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int pack_tiles(int keys) { return (keys + kPkKeys - 1) / kPkKeys; }
-// number of splits of T key tiles at c tiles each, at least one and at most `most`
-__device__ __forceinline__ int pack_splits(int T, int c, int most) { return max(1, min(most, pack_div(T, c))); }
-
-struct PackItem {
-  int q0, q_end;    // first token of the item, end of its sequence (rows of Q)
-  int t0, off;      // its index in the sequence; causal: token t sees keys <= t + off
-  int k0, lk;       // first key row, keys
-  int lo, hi;       // key tiles [lo, hi)
-  int head;         // key/value head
-  int slot;         // where a partial result goes; -1: the item finishes its rows
-  bool prefix;
-};
-
-// Block-wide inclusive scan of v (every thread calls it); total to *total.
-template <int WARPS>
-__device__ __forceinline__ int pack_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += t;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const int x = warp_sums[w];
-    if (w < warp) before += x;
-    all += x;
-  }
-  *total = all;
-  return s + before;
+// Splits of T key tiles, c tiles each and at most `most`.  Rows that fit one row tile
+// (narrow) have two streams to feed: at least two splits, where these are long enough.
+__device__ __forceinline__ int pack_splits(int T, bool narrow, int c, int most) {
+  if (narrow) c = min(c, max(kPkSplitKeys, pack_div(T, 2)));
+  return max(1, min(most, pack_div(T, c)));
+}
+// Items of `rows` tokens over T key tiles in ns splits.
+__device__ __forceinline__ int pack_count(int rows, int TQ, int ns) {
+  return rows <= TQ ? (rows > 0 ? pack_div(ns, 2) : 0) : pack_div(rows, 2 * TQ) * ns;
 }
 
-// Finds this CTA's item.  Every thread reads a share of the sequence table, so
-// that lengths stay on the device; false: no item (the grid is an upper bound).
-template <int NQ, int WARPS>
-__device__ bool pack_find(const PackParams& p, PackItem* shared_item, int* warp_sums, int* found) {
-  constexpr int T = 32 * WARPS;
-  const int TT = NQ * p.TQ;
-  if (threadIdx.x == 0) *found = 0;
-  if constexpr (NQ == 2) {
-    // one item per row tile pair, the last rows of the last sequence first: with
-    // the causal rule the long items start first
-    const int x = blockIdx.x;
-    int run = 0;
-    for (int base = 0; base < p.n; base += T) {
-      const int i = p.n - 1 - base - (int)threadIdx.x;
-      const PackSeq s = i >= 0 ? pack_seq(p, i) : PackSeq{0, 0, 0, 0};
-      const int mine = pack_div(s.lq, TT);
-      int total;
-      const int incl = pack_scan<WARPS>(mine, warp_sums, &total);
-      const int r = x - run - (incl - mine);
-      if (r >= 0 && r < mine) {
-        const int tile = mine - 1 - r;
-        PackItem it;
-        it.t0 = tile * TT;
-        it.q0 = s.q0 + it.t0;
-        it.q_end = s.q0 + s.lq;
-        it.off = s.lk - s.lq;
-        it.k0 = s.k0;
-        it.lk = s.lk;
-        it.lo = 0;
-        it.hi = pack_tiles(s.lk);
-        it.head = blockIdx.y;
-        it.slot = -1;
-        it.prefix = false;
-        *shared_item = it;
-        *found = 1;
-      }
-      run += total;
-      if (x < run) break;
+struct PackItem {
+  int q0, q_end;         // first token of the item, end of its sequence (rows of Q)
+  int t0, off;           // its index in the sequence; causal: token t sees keys <= t + off
+  int k0, lk;            // first key row, keys
+  int lo[2], nt[2];      // first key tile and number of key tiles of each stream
+  int slot[2];           // where a stream's partial result goes; -1: it finishes its rows; -2: no rows
+  int head;              // key/value head
+  int prefix;            // keys of the prefix (no causal rule)
+  int narrow;            // both streams have the item's rows and keys of their own
+  int stop;              // no further item
+};
+
+// What a CTA works out once from the sequence table: the number of items per
+// key/value head, and for up to 128 chunks of sequences the items before each.
+constexpr int kPkChunks = 128;
+struct PackTable {
+  unsigned long long work;
+  int longest;
+  int c, np, pi;           // tiles per split, prefix splits, prefix items
+  int total;               // items of a head
+  int before[kPkChunks + 1];
+};
+
+// Splits and items of a sequence.
+__device__ __forceinline__ int pack_seq_splits(const PackParams& p, const PackSeq& s, int c) {
+  return pack_splits(pack_tiles(s.lk), s.lq <= p.TQ, c, p.max_ns);
+}
+__device__ __forceinline__ int pack_seq_items(const PackParams& p, const PackSeq& s, int c) {
+  if (p.Lp && s.lk == 0) return 0;   // behind a prefix a sequence may have no keys of its own
+  return pack_count(s.lq, p.TQ, pack_seq_splits(p, s, c));
+}
+// Steps of a CTA over T key tiles for `rows` tokens.
+__device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, int rows, int T) {
+  if (rows <= 0) return 0;
+  return rows <= p.TQ ? (T + 1) / 2 : (unsigned long long)pack_div(rows, 2 * p.TQ) * T;
+}
+
+// Every thread reads a share of the table, so that lengths stay on the device.
+template <int THREADS>
+__device__ void pack_prepare(const PackParams& p, PackTable& tb) {
+  const int tid = threadIdx.x;
+  if (tid == 0) tb.work = 0, tb.longest = 0, tb.np = 0, tb.pi = 0, tb.c = 0x7FFFFFFF;
+  for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0;
+  const PackSeq mine = tid < p.n ? pack_seq(p, tid) : PackSeq{0, 0, 0, 0};   // read once where it covers the table
+  __syncthreads();
+  if (p.part) {
+    // the split length c follows from the work: a CTA's share of it, or a third of
+    // that where it is long, so that uneven items still end together
+    unsigned long long w = 0;
+    int l = 0;
+    for (int i = tid; i < p.n; i += THREADS) {
+      const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
+      const int t = pack_tiles(s.lk);
+      w += pack_steps(p, s.lq, t);
+      if (s.lq) l = max(l, t);
     }
-  } else {
-    // items of one key/value head: prefix tiles x splits, then each sequence's
-    // tiles x splits; the split length c follows from the total work, so that
-    // the items fill the CTA slots
-    __shared__ unsigned long long work;
-    __shared__ int items, longest;
-    if (threadIdx.x == 0) work = 0, items = 0, longest = 0;
-    __syncthreads();
-    {
-      unsigned long long w = 0;
-      int m = 0, l = 0;
-      for (int i = threadIdx.x; i < p.n; i += T) {
-        const PackSeq s = pack_seq(p, i);
-        const int a = pack_div(s.lq, TT), t = pack_tiles(s.lk);
-        w += (unsigned long long)a * t;
-        m += a;
-        if (a) l = max(l, t);
-      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      m = __reduce_add_sync(0xffffffffu, m);
-      l = __reduce_max_sync(0xffffffffu, l);
-      if ((threadIdx.x & 31) == 0) {
-        atomicAdd(&work, w);
-        atomicAdd(&items, m);
-        atomicMax(&longest, l);
-      }
+    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    l = __reduce_max_sync(0xffffffffu, l);
+    if ((tid & 31) == 0 && w) {
+      atomicAdd(&tb.work, w);
+      atomicMax(&tb.longest, l);
     }
     __syncthreads();
-    const PackSeq all = p.Lp ? pack_all(p) : PackSeq{0, 0, 0, 0};
-    const int pa = pack_div(all.lq, TT), pt = pack_tiles(p.Lp);
-    const int slots = max(1, kPkSlots / p.Hkv);          // of one head
-    const int n_items = items + pa, share = 2 * n_items <= slots ? slots - n_items : slots;
-    const unsigned long long n_work = work + (unsigned long long)pa * pt;
-    int c = (int)((n_work + share - 1) / share);
-    c = max(max(c, kPkSplitKeys), pack_div(longest, p.max_ns));
-    if (p.Lp) c = max(c, pack_div(pt, p.max_np));
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.chunk) *p.chunk = c;
-    const int np = p.Lp ? pack_splits(pt, c, p.max_np) : 0;
-    const int head = blockIdx.x % p.Hkv;
-    int x = blockIdx.x / p.Hkv;
-    if (x < pa * np) {
-      if (threadIdx.x == 0) {
-        const int tile = x / np, sp = x % np, per = pack_div(pt, np);
-        PackItem it;
-        it.t0 = tile * TT;
-        it.q0 = all.q0 + it.t0;
-        it.q_end = all.q0 + all.lq;
-        it.off = 0;
-        it.k0 = 0;
-        it.lk = p.Lp;
-        it.lo = min(sp * per, pt);
-        it.hi = min(it.lo + per, pt);
-        it.head = head;
-        it.slot = sp;
-        it.prefix = true;
-        *shared_item = it;
-        *found = 1;
+    if (tid == 0) {
+      const int pt = pack_tiles(p.Lp), rows = p.Lp ? pack_all(p).lq : 0;
+      const unsigned long long work = (tb.work + pack_steps(p, rows, pt)) * p.Hkv;
+      int c = (int)((work + kPkSMs - 1) / kPkSMs);
+      if (c > kPkFine) c = max(kPkFine, pack_div(c, 3));
+      c = max(max(c, kPkSplitKeys), pack_div(tb.longest, p.max_ns));
+      if (p.Lp) c = max(c, pack_div(pt, p.max_np));
+      tb.c = c;
+      if (p.Lp) {
+        tb.np = pack_splits(pt, rows <= p.TQ, c, p.max_np);
+        tb.pi = pack_count(rows, p.TQ, tb.np);
       }
-    } else {
-      x -= pa * np;
-      int run = 0;
-      for (int base = 0; base < p.n; base += T) {
-        const int i = base + (int)threadIdx.x;
-        const PackSeq s = i < p.n ? pack_seq(p, i) : PackSeq{0, 0, 0, 0};
-        const int a = pack_div(s.lq, TT), t = pack_tiles(s.lk), ns = pack_splits(t, c, p.max_ns);
-        const int mine = (p.Lp && t == 0) ? 0 : a * ns;  // behind a prefix a sequence may have no keys of its own
-        int total;
-        const int incl = pack_scan<WARPS>(mine, warp_sums, &total);
-        const int r = x - run - (incl - mine);
-        if (r >= 0 && r < mine) {
-          const int tile = r / ns, sp = r % ns, per = pack_div(t, ns);
-          PackItem it;
-          it.t0 = tile * TT;
-          it.q0 = s.q0 + it.t0;
-          it.q_end = s.q0 + s.lq;
-          it.off = s.lk - s.lq;
-          it.k0 = s.k0;
-          it.lk = s.lk;
-          it.lo = min(sp * per, t);
-          it.hi = min(it.lo + per, t);
-          it.head = head;
-          it.slot = (p.Lp || ns > 1) ? np + sp : -1;
-          it.prefix = false;
-          *shared_item = it;
-          *found = 1;
-        }
-        run += total;
-        if (x < run) break;
-      }
+      if (blockIdx.x == 0) *p.chunk = c;
     }
+    __syncthreads();
+  }
+  const int cs = pack_div(p.n, kPkChunks), c = tb.c;
+  for (int i = tid; i < p.n; i += THREADS) {
+    const int m = pack_seq_items(p, i < THREADS ? mine : pack_seq(p, i), c);
+    if (m) atomicAdd(&tb.before[i / cs + 1], m);
   }
   __syncthreads();
-  return *found != 0;
+  if (tid < 32) {   // inclusive sums of 4 chunks a lane
+    int v[kPkChunks / 32], s = 0;
+#pragma unroll
+    for (int j = 0; j < kPkChunks / 32; ++j) v[j] = s += tb.before[1 + tid * (kPkChunks / 32) + j];
+    int run = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, run, o);
+      if (tid >= o) run += t;
+    }
+#pragma unroll
+    for (int j = 0; j < kPkChunks / 32; ++j) tb.before[1 + tid * (kPkChunks / 32) + j] = run - s + v[j];
+    if (tid == 31) tb.total = run + tb.pi;
+  }
+  __syncthreads();
+}
+
+// Item number `id` (a warp together); stop past the last one.  A head's items follow
+// one another: the prefix, then the last rows of the last sequence first (with the
+// causal rule the long items start first).
+__device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& tb, int id, PackItem& it) {
+  const int lane = threadIdx.x & 31;
+  it.stop = 1;
+  if (id / p.Hkv >= tb.total) return;   // total * Hkv items in all
+  it.stop = 0;
+  it.head = id / tb.total;
+  int x = id % tb.total;
+  PackSeq s{0, 0, 0, 0};
+  int ns, base = -1;                    // splits; slot of the first one
+  it.prefix = x < tb.pi;
+  if (it.prefix) {
+    s = pack_all(p);
+    ns = tb.np;
+    base = 0;
+  } else {
+    x = tb.total - 1 - x;
+    // the chunk, then the sequence in it
+    int ch = 0;
+#pragma unroll
+    for (int j = 0; j < kPkChunks / 32; ++j) ch += __popc(__ballot_sync(0xffffffffu, tb.before[1 + j * 32 + lane] <= x));
+    x -= tb.before[ch];
+    const int cs = pack_div(p.n, kPkChunks), end = min(p.n, (ch + 1) * cs);
+    for (int b = ch * cs; b < end; b += 32) {
+      const int i = b + lane;
+      const PackSeq mine = i < end ? pack_seq(p, i) : PackSeq{0, 0, 0, 0};
+      const int m = pack_seq_items(p, mine, tb.c);
+      int run = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += t;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, run > x);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        s.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+        s.lq = __shfl_sync(0xffffffffu, mine.lq, src);
+        s.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+        s.lk = __shfl_sync(0xffffffffu, mine.lk, src);
+        x -= __shfl_sync(0xffffffffu, run - m, src);
+        break;
+      }
+      x -= __shfl_sync(0xffffffffu, run, 31);
+    }
+    ns = pack_seq_splits(p, s, tb.c);
+    if (p.Lp || ns > 1) base = tb.np;
+  }
+  const int T = pack_tiles(s.lk), per = pack_div(T, ns);
+  it.narrow = s.lq <= p.TQ;
+  const int tile = it.narrow ? 0 : x / ns;
+  it.t0 = tile * 2 * p.TQ;
+  it.q0 = s.q0 + it.t0;
+  it.q_end = s.q0 + s.lq;
+  it.off = s.lk - s.lq;
+  it.k0 = s.k0;
+  it.lk = s.lk;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int sp = it.narrow ? 2 * x + g : x % ns, first = it.narrow ? 0 : g * p.TQ;
+    const int tokens = min(p.TQ, it.q_end - it.q0 - first);
+    int lo = min(sp * per, T), hi = min(lo + per, T);
+    // key tiles up to the last key that the tile's last token sees
+    if (p.causal && !it.prefix) hi = min(hi, pack_tiles(max(0, min(s.lk, it.t0 + first + tokens + it.off))));
+    const bool live = tokens > 0 && sp < ns;
+    it.lo[g] = lo;
+    it.nt[g] = live ? max(0, hi - lo) : 0;
+    it.slot[g] = !live ? -2 : (base < 0 ? -1 : base + sp);
+  }
+}
+
+// ---------------------------------------------------------------- cluster launch control
+// Asks for a block that has not started; the answer (16 bytes) arrives at `bar`.
+__device__ __forceinline__ void clc_request(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The block taken over, or -1 when none was left.
+__device__ __forceinline__ int clc_answer(const void* answer) {
+  uint32_t ok, x = 0;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? (int)x : -1;
 }
 
 // One row over keys [lo, hi), a warp together: lane holds D / 32 neighbouring
@@ -330,56 +374,53 @@ __device__ __noinline__ void packed_exact_row(const __nv_bfloat16* q, const __nv
 
 __device__ __forceinline__ float pack_lse(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
-template <int D, int NQ>
-__global__ void __launch_bounds__(PackCfg<D, NQ>::THREADS, NQ == 1 ? 2 : 1)
+template <int D>
+__global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKp,
                        const __grid_constant__ CUtensorMap tmVp, const PackParams p) {
-  using C = PackCfg<D, NQ>;
+  using C = PackCfg<D>;
+  constexpr int NQ = 2;   // streams
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // full/empty: a ring slot; sfull[g]: S_g complete; pfull[g]: P_g written; odone[g]: O_g complete
-  __shared__ uint64_t bar_q, bar_full[C::RING], bar_empty[C::RING], bar_sfull[NQ], bar_pfull[NQ], bar_odone[NQ],
-      bar_drain;
+  // full/empty: a ring slot; qfull/qempty[g]: the tile Q_g; sfull[g]: S_g complete; pfull[g]: P_g written;
+  // odone[g]: O_g complete; ifull/iempty: an item slot; clc: an answer of the launch control
+  __shared__ uint64_t bar_full[C::RING], bar_empty[C::RING], bar_qfull[NQ], bar_qempty[NQ], bar_sfull[NQ], bar_pfull[NQ],
+      bar_odone[NQ], bar_ifull[kPkItems], bar_iempty[kPkItems], bar_clc, bar_drain;
+  __shared__ __align__(16) uint4 clc;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ int never_abort, found;
-  __shared__ int warp_sums[C::WARPS];
-  __shared__ PackItem item;
+  __shared__ int never_abort;
+  __shared__ PackTable table;
+  __shared__ PackItem items[kPkItems];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (!pack_find<NQ, C::WARPS>(p, &item, warp_sums, &found)) return;
-  const PackItem it = item;
-
-  // key tiles of each row tile: up to the last key that its last token sees
-  int nt[NQ];
-  int most = 0;
-#pragma unroll
-  for (int g = 0; g < NQ; ++g) {
-    const int first = g * p.TQ, tokens = min(p.TQ, it.q_end - it.q0 - first);
-    int hi = it.hi;
-    if (p.causal && !it.prefix) hi = min(hi, pack_tiles(max(0, min(it.lk, it.t0 + first + tokens + it.off))));
-    nt[g] = tokens > 0 ? max(0, hi - it.lo) : 0;
-    most = max(most, nt[g]);
-  }
+  constexpr int TMA_WARP = 4 * NQ, MMA_WARP = 4 * NQ + 1;
+  pack_prepare<C::THREADS>(p, table);
+  if ((int)blockIdx.x / p.Hkv >= table.total) return;   // the grid is an upper bound
 
   if (threadIdx.x == 0) {
-    mbar_init(&bar_q, 1);
     for (int s = 0; s < C::RING; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], 1);
     }
     for (int g = 0; g < NQ; ++g) {
+      mbar_init(&bar_qfull[g], 1);
+      mbar_init(&bar_qempty[g], 1);
       mbar_init(&bar_sfull[g], 1);
       mbar_init(&bar_pfull[g], 4);  // one arrival per softmax warp
       mbar_init(&bar_odone[g], 1);
     }
+    for (int s = 0; s < kPkItems; ++s) {
+      mbar_init(&bar_ifull[s], 1);
+      mbar_init(&bar_iempty[s], C::READERS);
+    }
+    mbar_init(&bar_clc, 1);
     mbar_init(&bar_drain, 1);
     abort_flag = 0;
     never_abort = 0;
     fence_barrier_init();
   }
-  constexpr int TMA_WARP = 4 * NQ, MMA_WARP = 4 * NQ + 1;
   if (warp == MMA_WARP) {
     tmem_alloc(&tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
@@ -389,249 +430,337 @@ __global__ void __launch_bounds__(PackCfg<D, NQ>::THREADS, NQ == 1 ? 2 : 1)
   tc_fence_after();
   const uint32_t tbase = tmem_slot;
 
-  if (warp == TMA_WARP) {
-    // ================= loads: Q, then K(0), V(0), K(1), V(1), ... =================
-    const bool leader = elect_one();
-    const CUtensorMap* mk = it.prefix ? &tmKp : &tmK;
-    const CUtensorMap* mv = it.prefix ? &tmVp : &tmV;
-    int issued = 0;
-    bool ok = true, q_issued = false;
-    if (most > 0) {
+  // the k-th item, for the warps that read items; done_item when it is not read any more
+  auto next_item = [&](int k) {
+    return warp_wait(&bar_ifull[k % kPkItems], (uint32_t)(k / kPkItems) & 1u, &abort_flag, p.limit_ns);
+  };
+  auto done_item = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_iempty[k % kPkItems]);
+  };
+  if (warp >= 4 * NQ) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
+    if (warp == TMA_WARP) {
+      // ================= items and loads: Q, then K(0), V(0), K(1), V(1), ... =================
+      const bool leader = elect_one();
       if (leader) {
         prefetch_tensormap(&tmQ);
-        prefetch_tensormap(mk);
-        prefetch_tensormap(mv);
-        const uint32_t qbytes = (uint32_t)(p.G * p.TQ * 128);
-        int live = 0;
-        for (int g = 0; g < NQ; ++g) live += nt[g] > 0;
-        mbar_arrive_expect_tx(&bar_q, live * C::NATOM * qbytes);
-        for (int g = 0; g < NQ; ++g)
-          if (nt[g] > 0)
-            for (int a = 0; a < C::NATOM; ++a)
-              tma_load_4d(sm + g * C::TILE_BYTES + a * 128 * 128, &tmQ, &bar_q, a * 64, 0, it.q0 + g * p.TQ, it.head);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
       }
-      q_issued = true;
-      for (int m = 0; ok && m < 2 * most; ++m) {
-        const int slot = m % C::RING;
-        if (m >= C::RING) {
-          ok = warp_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, p.limit_ns);
+      int m = 0;                 // loads into the ring so far
+      int uq[NQ];                // loads of each Q tile
+  #pragma unroll
+      for (int g = 0; g < NQ; ++g) uq[g] = 0;
+      bool ok = true, asked = false;
+      int id = blockIdx.x;
+      int k = 0;
+      for (;; ++k) {
+        PackItem it;
+        pack_item(p, table, id, it);
+        if (k >= kPkItems) {
+          ok = warp_wait(&bar_iempty[k % kPkItems], (uint32_t)(k / kPkItems - 1) & 1u, &abort_flag, p.limit_ns);
           if (!ok) break;
         }
         if (leader) {
-          uint8_t* dst = sm + C::OFF_RING + slot * C::TILE_BYTES;
-          const int row = it.k0 + (it.lo + (m >> 1)) * kPkKeys;
-          mbar_arrive_expect_tx(&bar_full[slot], C::TILE_BYTES);
-          for (int a = 0; a < C::NATOM; ++a)
-            tma_load_4d(dst + a * 128 * 128, (m & 1) ? mv : mk, &bar_full[slot], a * 64, row, it.head, 0);
+          items[k % kPkItems] = it;
+          mbar_arrive(&bar_ifull[k % kPkItems]);
+          if (!it.stop) {        // ask for the next one now: the answer comes under this item's loads
+            mbar_arrive_expect_tx(&bar_clc, 16);
+            clc_request(&clc, &bar_clc);
+          }
         }
         __syncwarp();
-        ++issued;
-      }
-    }
-    if (leader) {
-      if (!ok) {
-        abort_flag = 1;
-        report_error(-6);
-      }
-      // drain: every issued load lands before the CTA may exit
-      if (q_issued) mbar_wait(&bar_q, 0, &never_abort, p.limit_ns);
-      for (int m = max(0, issued - C::RING); m < issued; ++m)
-        mbar_wait(&bar_full[m % C::RING], (uint32_t)(m / C::RING) & 1u, &never_abort, p.limit_ns);
-    }
-    __syncwarp();
-  } else if (warp == MMA_WARP) {
-    // ================= MMA: per key tile j and row tile g, O_g += P_g(j) V(j), then S_g(j+1) =================
-    const uint32_t sbase = smem_u32(sm);
-    const bool leader = elect_one();
-    bool ok = true;
-    auto wait_full = [&](int m) {
-      return warp_wait(&bar_full[m % C::RING], (uint32_t)(m / C::RING) & 1u, &abort_flag, p.limit_ns);
-    };
-    auto issue_s = [&](int g, int j) {  // S_g = Q_g K(j)^T
-      const int slot = (2 * j) % C::RING;
-      const uint64_t dq = smem_desc(sbase + g * C::TILE_BYTES, 16, 1024, SW_128B);
-      const uint64_t dk = smem_desc(sbase + C::OFF_RING + slot * C::TILE_BYTES, 16, 1024, SW_128B);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t step = (uint64_t)(((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4);
-        mma_ss<KIND_F16>(tbase + C::S_COL + 128 * g, dq + step, dk + step, C::IDESC_S, kk > 0 ? 1u : 0u);
-      }
-      mma_commit(&bar_sfull[g]);
-    };
-    if (most > 0) {
-      ok = warp_wait(&bar_q, 0, &abort_flag, p.limit_ns) && wait_full(0);
-      if (ok) {
-        tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int g = 0; g < NQ; ++g)
-            if (nt[g] > 0) issue_s(g, 0);
-          mma_commit(&bar_empty[0]);
-        }
-        __syncwarp();
-      }
-      for (int j = 0; ok && j < most; ++j) {
-        const int vslot = (2 * j + 1) % C::RING;
-        ok = wait_full(2 * j + 1);
-        if (!ok) break;
-        // V rows past the sequence's end belong to somebody else: zero them
-        const int left = it.lk - (it.lo + j) * kPkKeys;
-        if (left < kPkKeys) {
-          uint8_t* vt = sm + C::OFF_RING + vslot * C::TILE_BYTES;
-          for (int a = 0; a < C::NATOM; ++a)
-            for (int b = left * 128 + lane * 16; b < kPkKeys * 128; b += 512)
-              *reinterpret_cast<uint4*>(vt + a * 128 * 128 + b) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
+        if (it.stop) break;
+        asked = true;
+        const CUtensorMap* mk = it.prefix ? &tmKp : &tmK;
+        const CUtensorMap* mv = it.prefix ? &tmVp : &tmV;
+  #pragma unroll
+        for (int g = 0; g < NQ; ++g) {
+          if (it.nt[g] == 0) continue;
+          if (uq[g] > 0) {
+            ok = warp_wait(&bar_qempty[g], (uint32_t)(uq[g] - 1) & 1u, &abort_flag, p.limit_ns);
+            if (!ok) break;
+          }
+          if (leader) {
+            mbar_arrive_expect_tx(&bar_qfull[g], (uint32_t)(C::NATOM * p.G * p.TQ * 128));
+            for (int a = 0; a < C::NATOM; ++a)
+              tma_load_4d(sm + g * C::TILE_BYTES + a * 128 * 128, &tmQ, &bar_qfull[g], a * 64, 0,
+                          it.q0 + (it.narrow ? 0 : g * p.TQ), it.head);
+          }
           __syncwarp();
+          ++uq[g];
         }
-        bool k_ready = false;
-        const int last = (NQ == 2 && nt[NQ - 1] > j) ? NQ - 1 : 0;         // last row tile that uses V(j)
-        const int last_s = (NQ == 2 && nt[NQ - 1] > j + 1) ? NQ - 1 : 0;   // last row tile that uses K(j+1)
+        if (!ok) break;
+        // shared key tiles: K(j), V(j); of its own for each stream: K_0(j), K_1(j), V_0(j), V_1(j)
+        const int most = max(it.nt[0], it.nt[1]);
+        auto load = [&](const CUtensorMap* map, int tile) {
+          const int slot = m % C::RING;
+          if (m >= C::RING &&
+              !warp_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, p.limit_ns))
+            return false;
+          if (leader) {
+            uint8_t* dst = sm + C::OFF_RING + slot * C::TILE_BYTES;
+            mbar_arrive_expect_tx(&bar_full[slot], C::TILE_BYTES);
+            for (int a = 0; a < C::NATOM; ++a)
+              tma_load_4d(dst + a * 128 * 128, map, &bar_full[slot], a * 64, it.k0 + tile * kPkKeys, it.head, 0);
+          }
+          __syncwarp();
+          ++m;
+          return true;
+        };
+        for (int j = 0; ok && j < most; ++j) {
+          if (!it.narrow) {
+            ok = load(mk, it.lo[0] + j) && load(mv, it.lo[0] + j);
+          } else {
+            const bool b1 = j < it.nt[1];
+            ok = load(mk, it.lo[0] + j) && (!b1 || load(mk, it.lo[1] + j)) && load(mv, it.lo[0] + j) &&
+                 (!b1 || load(mv, it.lo[1] + j));
+          }
+        }
+        if (!ok) break;
+        ok = warp_wait(&bar_clc, (uint32_t)k & 1u, &abort_flag, p.limit_ns);
+        if (!ok) break;
+        asked = false;
+        const int next = clc_answer(&clc);
+        fence_proxy_async_smem();   // read before the next answer overwrites it
+        id = next < 0 ? 0x7FFFFFFF : next;
+        __syncwarp();
+      }
+      if (leader) {
+        if (!ok) {
+          abort_flag = 1;
+          report_error(-6);
+        }
+        // drain: every issued load and answer lands before the CTA may exit
+        if (asked) mbar_wait(&bar_clc, (uint32_t)k & 1u, &never_abort, p.limit_ns);
+  #pragma unroll
+        for (int g = 0; g < NQ; ++g)
+          if (uq[g] > 0) mbar_wait(&bar_qfull[g], (uint32_t)(uq[g] - 1) & 1u, &never_abort, p.limit_ns);
+        for (int j = max(0, m - C::RING); j < m; ++j)
+          mbar_wait(&bar_full[j % C::RING], (uint32_t)(j / C::RING) & 1u, &never_abort, p.limit_ns);
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      // ================= MMA: per key tile j and row tile g, O_g += P_g(j) V(j), then S_g(j+1) =================
+      const uint32_t sbase = smem_u32(sm);
+      const bool leader = elect_one();
+      bool ok = true;
+      int m = 0;                 // ring position of this item's first load
+      int uq[NQ], up[NQ];        // Q tiles and P tiles used
+#pragma unroll
+      for (int g = 0; g < NQ; ++g) uq[g] = 0, up[g] = 0;
+      auto wait_full = [&](int at) {
+        return warp_wait(&bar_full[at % C::RING], (uint32_t)(at / C::RING) & 1u, &abort_flag, p.limit_ns);
+      };
+      // S_g = Q_g K^T; the K tile is free after its last reader, Q_g after the item's last tile
+      auto issue_s = [&](int g, int at, bool free_k, bool free_q) {
+        const int slot = at % C::RING;
+        const uint64_t dq = smem_desc(sbase + g * C::TILE_BYTES, 16, 1024, SW_128B);
+        const uint64_t dk = smem_desc(sbase + C::OFF_RING + slot * C::TILE_BYTES, 16, 1024, SW_128B);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = (uint64_t)(((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4);
+          mma_ss<KIND_F16>(tbase + C::S_COL + 128 * g, dq + step, dk + step, C::IDESC_S, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&bar_sfull[g]);
+        if (free_k) mma_commit(&bar_empty[slot]);
+        if (free_q) mma_commit(&bar_qempty[g]);
+      };
+      for (int k = 0; ok; ++k) {
+        ok = next_item(k);
+        if (!ok) break;
+        const PackItem& it = items[k % kPkItems];
+        const int n0 = it.nt[0], n1 = it.nt[1], most = max(n0, n1);
+        const bool stop = it.stop, narrow = it.narrow;
+        const int keys0 = it.lk - it.lo[0] * kPkKeys, keys1 = it.lk - it.lo[1] * kPkKeys;   // from the first tile on
+        done_item(k);
+        if (stop) break;
+        if (most == 0) continue;
+        // ring position of K_g(j) and V_g(j); narrow: n0 >= n1, four loads a step while both run
+        auto at_k = [&](int g, int j) {
+          return narrow ? m + (j < n1 ? 4 * j + g : 2 * (j + n1)) : m + 2 * j;
+        };
+        auto at_v = [&](int g, int j) {
+          return narrow ? m + (j < n1 ? 4 * j + 2 + g : 2 * (j + n1) + 1) : m + 2 * j + 1;
+        };
+        // the last stream that reads a tile of step j frees it
+        auto frees = [&](int g, int j) { return narrow || g == (n1 > j ? 1 : 0); };
 #pragma unroll
         for (int g = 0; g < NQ; ++g) {
-          if (j >= nt[g]) continue;
-          ok = warp_wait(&bar_pfull[g], (uint32_t)j & 1u, &abort_flag, p.limit_ns);
-          if (ok && j + 1 < nt[g] && !k_ready) {
-            ok = wait_full(2 * j + 2);
-            k_ready = true;
-          }
+          if (!ok || (g ? n1 : n0) == 0) continue;
+          ok = wait_full(at_k(g, 0)) && warp_wait(&bar_qfull[g], (uint32_t)(uq[g]++) & 1u, &abort_flag, p.limit_ns);
           if (!ok) break;
           tc_fence_after();
-          if (leader) {
-            const uint64_t dv = smem_desc(sbase + C::OFF_RING + vslot * C::TILE_BYTES, 128 * 128, 1024, SW_128B);
-#pragma unroll
-            for (int kk = 0; kk < kPkKeys / 16; ++kk)
-              mma_ts<KIND_F16>(tbase + C::O_COL + D * g, tbase + C::S_COL + 128 * g + 8 * kk,
-                               dv + (uint64_t)((kk * 16 * 128) >> 4), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 == nt[g]) mma_commit(&bar_odone[g]);
-            if (g == last) mma_commit(&bar_empty[vslot]);
-            if (j + 1 < nt[g]) {
-              issue_s(g, j + 1);
-              if (g == last_s) mma_commit(&bar_empty[(2 * j + 2) % C::RING]);
-            }
-          }
+          if (leader) issue_s(g, at_k(g, 0), frees(g, 0), (g ? n1 : n0) == 1);
           __syncwarp();
         }
+        for (int j = 0; ok && j < most; ++j) {
+#pragma unroll
+          for (int g = 0; g < NQ; ++g) {
+            const int n = g ? n1 : n0;
+            if (!ok || j >= n) continue;
+            const int va = at_v(g, j), vslot = va % C::RING;
+            ok = wait_full(va);
+            if (!ok) break;
+            // V rows past the sequence's end belong to somebody else: zero them
+            const int left = (g ? keys1 : keys0) - j * kPkKeys;
+            if (left < kPkKeys && (g == 0 || narrow || n0 <= j)) {
+              uint8_t* vt = sm + C::OFF_RING + vslot * C::TILE_BYTES;
+              for (int a = 0; a < C::NATOM; ++a)
+                for (int b = left * 128 + lane * 16; b < kPkKeys * 128; b += 512)
+                  *reinterpret_cast<uint4*>(vt + a * 128 * 128 + b) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            ok = warp_wait(&bar_pfull[g], (uint32_t)(up[g]++) & 1u, &abort_flag, p.limit_ns) &&
+                 (j + 1 >= n || wait_full(at_k(g, j + 1)));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t dv = smem_desc(sbase + C::OFF_RING + vslot * C::TILE_BYTES, 128 * 128, 1024, SW_128B);
+#pragma unroll
+              for (int kk = 0; kk < kPkKeys / 16; ++kk)
+                mma_ts<KIND_F16>(tbase + C::O_COL + D * g, tbase + C::S_COL + 128 * g + 8 * kk,
+                                 dv + (uint64_t)((kk * 16 * 128) >> 4), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+              if (j + 1 == n) mma_commit(&bar_odone[g]);
+              if (frees(g, j)) mma_commit(&bar_empty[vslot]);
+              if (j + 1 < n) issue_s(g, at_k(g, j + 1), frees(g, j + 1), j + 2 == n);
+            }
+            __syncwarp();
+          }
+        }
+        m += narrow ? 2 * (n0 + n1) : 2 * most;
       }
-    }
-    if (leader) {
-      if (!ok) {
-        abort_flag = 1;
-        report_error(-6);
+      if (leader) {
+        if (!ok) {
+          abort_flag = 1;
+          report_error(-6);
+        }
+        // drain: every issued MMA completes before TMEM is released
+        mma_commit(&bar_drain);
+        mbar_wait(&bar_drain, 0, &never_abort, p.limit_ns);
       }
-      // drain: every issued MMA completes before TMEM is released
-      mma_commit(&bar_drain);
-      mbar_wait(&bar_drain, 0, &never_abort, p.limit_ns);
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ================= softmax, rescale, epilogue: thread = row =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     const int g = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int tok = g * p.TQ + row / p.G;                // token of the item
-    const int head = it.head * p.G + row % p.G;
-    const bool valid = row < p.TQ * p.G && it.q0 + tok < it.q_end;
-    const bool warp_live = __any_sync(0xffffffffu, valid);
-    // keys [0, seen) of the sequence are visible to this row
-    const int seen = (p.causal && !it.prefix) ? max(0, min(it.lk, it.t0 + tok + it.off + 1)) : it.lk;
-    const int my_nt = NQ == 2 ? (g ? nt[NQ - 1] : nt[0]) : nt[0];
+    const int row_tok = row / p.G, row_head = row % p.G;
+    const bool row_in = row < p.TQ * p.G;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_addr = tbase + lanes + C::S_COL + 128 * g, o_addr = tbase + lanes + C::O_COL + D * g;
     const float sc = p.scale_log2;
-    float m_use = -INFINITY, l_run = 0.f;
+    int us = 0, uo = 0;        // S tiles and O tiles read
     bool ok = true;
-    for (int j = 0; j < my_nt; ++j) {
-      ok = warp_wait(&bar_sfull[g], (uint32_t)j & 1u, &abort_flag, p.limit_ns);
-      if (!ok) break;
-      tc_fence_after();
-      if (warp_live) {
-        uint32_t sv[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-        const int nv = seen - (it.lo + j) * kPkKeys;      // visible columns of this tile
-        if (__any_sync(0xffffffffu, nv < kPkKeys)) {
-#pragma unroll
-          for (int u = 0; u < 128; ++u)
-            if (u >= nv) sv[u] = 0xFF800000u;             // -inf
-        }
-        const float* f = reinterpret_cast<const float*>(sv);
-        float t8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float a = fmaxf(f[i], f[i + 8]);
-#pragma unroll
-          for (int u = 16; u < 112; u += 16) a = fmax3(a, f[i + u], f[i + u + 8]);
-          t8[i] = fmax3(a, f[i + 112], f[i + 120]);
-        }
-        const float mx = fmaxf(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], fmax3(t8[5], t8[6], t8[7]))) * sc;
-        const bool grow = mx > m_use + kPkLazy;           // also the first finite maximum
-        if (__any_sync(0xffffffffu, grow)) {
-          const float alpha = grow ? ex2f(m_use - mx) : 1.f;   // 0 from -inf
-          if (grow) m_use = mx;
-          l_run *= alpha;
-          if (j > 0) {
-            const uint64_t a2 = f2pack(alpha, alpha);
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_addr + c, o);
-              tmem_wait_ld();
-              reg_fence32(o);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float x, y;
-                f2unpack(mul2(f2pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x, y);
-                o[i] = __float_as_uint(x);
-                o[i + 1] = __float_as_uint(y);
+    for (int k = 0; ok; ++k) {
+      ok = next_item(k);
+      const PackItem& it = items[k % kPkItems];
+      if (!ok || it.stop) break;
+      const int slot = it.slot[g];
+      const int tok = row_tok + (it.narrow ? 0 : g * p.TQ);   // token of the item
+      const bool valid = row_in && it.q0 + tok < it.q_end && slot > -2;
+      const bool warp_live = __any_sync(0xffffffffu, valid);
+      // keys [0, seen) of the sequence are visible to this row
+      const int seen = (p.causal && !it.prefix) ? max(0, min(it.lk, it.t0 + tok + it.off + 1)) : it.lk;
+      const int my_nt = it.nt[g], lo = it.lo[g], ahead = seen - lo * kPkKeys;
+      float m_use = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < my_nt; ++j) {
+        ok = warp_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, p.limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t sv[128];
+  #pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+          tmem_wait_ld();
+  #pragma unroll
+          for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+          const int nv = ahead - j * kPkKeys;               // visible columns of this tile
+          if (__any_sync(0xffffffffu, nv < kPkKeys)) {
+  #pragma unroll
+            for (int u = 0; u < 128; ++u)
+              if (u >= nv) sv[u] = 0xFF800000u;             // -inf
+          }
+          const float* f = reinterpret_cast<const float*>(sv);
+          float t8[8];
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float a = fmaxf(f[i], f[i + 8]);
+  #pragma unroll
+            for (int u = 16; u < 112; u += 16) a = fmax3(a, f[i + u], f[i + u + 8]);
+            t8[i] = fmax3(a, f[i + 112], f[i + 120]);
+          }
+          const float mx = fmaxf(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], fmax3(t8[5], t8[6], t8[7]))) * sc;
+          const bool grow = mx > m_use + kPkLazy;           // also the first finite maximum
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? ex2f(m_use - mx) : 1.f;   // 0 from -inf
+            if (grow) m_use = mx;
+            l_run *= alpha;
+            if (j > 0) {
+              const uint64_t a2 = f2pack(alpha, alpha);
+  #pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + c, o);
+                tmem_wait_ld();
+                reg_fence32(o);
+  #pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float x, y;
+                  f2unpack(mul2(f2pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x, y);
+                  o[i] = __float_as_uint(x);
+                  o[i + 1] = __float_as_uint(y);
+                }
+                tmem_st32(o_addr + c, o);
               }
-              tmem_st32(o_addr + c, o);
             }
           }
+          const float at = m_use == -INFINITY ? 0.f : m_use;  // nothing visible yet: exp2(-inf - 0) = 0
+          const uint64_t sc2 = f2pack(sc, sc), nm2 = f2pack(-at, -at);
+          uint64_t sum2[4] = {0, 0, 0, 0};
+          uint32_t pk[64];
+  #pragma unroll
+          for (int u = 0; u < 128; u += 2) {
+            float x0, x1;
+            f2unpack(fma2(f2pack(__uint_as_float(sv[u]), __uint_as_float(sv[u + 1])), sc2, nm2), x0, x1);
+            const float p0 = ex2f(x0), p1 = ex2f(x1);
+            sum2[(u >> 1) & 3] = add2(sum2[(u >> 1) & 3], f2pack(p0, p1));
+            const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
+            pk[u >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
+          }
+          tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          float a0, a1, b0, b1;
+          f2unpack(add2(sum2[0], sum2[1]), a0, a1);
+          f2unpack(add2(sum2[2], sum2[3]), b0, b1);
+          l_run += (a0 + a1) + (b0 + b1);
+          tmem_wait_st();
         }
-        const float at = m_use == -INFINITY ? 0.f : m_use;  // nothing visible yet: exp2(-inf - 0) = 0
-        const uint64_t sc2 = f2pack(sc, sc), nm2 = f2pack(-at, -at);
-        uint64_t sum2[4] = {0, 0, 0, 0};
-        uint32_t pk[64];
-#pragma unroll
-        for (int u = 0; u < 128; u += 2) {
-          float x0, x1;
-          f2unpack(fma2(f2pack(__uint_as_float(sv[u]), __uint_as_float(sv[u + 1])), sc2, nm2), x0, x1);
-          const float p0 = ex2f(x0), p1 = ex2f(x1);
-          sum2[(u >> 1) & 3] = add2(sum2[(u >> 1) & 3], f2pack(p0, p1));
-          const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
-          pk[u >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
-        }
-        tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-        float a0, a1, b0, b1;
-        f2unpack(add2(sum2[0], sum2[1]), a0, a1);
-        f2unpack(add2(sum2[2], sum2[3]), b0, b1);
-        l_run += (a0 + a1) + (b0 + b1);
-        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_pfull[g]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_pfull[g]);
-    }
-    if (ok && my_nt > 0) {
-      ok = warp_wait(&bar_odone[g], 0, &abort_flag, p.limit_ns);
-      tc_fence_after();
-    }
-    if (!ok) {
-      abort_flag = 1;
-      report_error(-6);
-    } else if (warp_live) {
-      const int from = it.lo * kPkKeys;                          // keys [from, to) were computed
-      const int to = min(it.lk, (it.lo + my_nt) * kPkKeys);
+      if (ok && my_nt > 0) {
+        ok = warp_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, p.limit_ns);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      if (!warp_live) {
+        done_item(k);
+        continue;
+      }
+      const int head = it.head * p.G + row_head;
+      const int from = lo * kPkKeys;                          // keys [from, to) were computed
+      const int to = min(it.lk, (lo + my_nt) * kPkKeys);
       const bool any = valid && seen > from && my_nt > 0;        // this row saw a key
-      const float inv = it.slot < 0 ? 1.0f / l_run : 1.0f;
+      const float inv = slot < 0 ? 1.0f / l_run : 1.0f;
       const long long tr = it.q0 + tok;
       __nv_bfloat16* orow = p.o + head * p.osH + tr * p.osL;
-      const long long R = (long long)p.Tq * p.Hkv * p.G, prow = it.slot * R + tr * (p.Hkv * p.G) + head;
-      float* part = it.slot < 0 ? nullptr : p.part + prow * D;
+      const long long R = (long long)p.Tq * p.Hkv * p.G, prow = slot * R + tr * (p.Hkv * p.G) + head;
+      float* part = slot < 0 ? nullptr : p.part + prow * D;
       float check = 0.f;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -648,7 +777,7 @@ __global__ void __launch_bounds__(PackCfg<D, NQ>::THREADS, NQ == 1 ? 2 : 1)
           o[i] = __float_as_uint(any ? x * inv : 0.f);
         }
         if (!valid) continue;
-        if (it.slot < 0) {
+        if (slot < 0) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t h[4];
@@ -667,7 +796,7 @@ __global__ void __launch_bounds__(PackCfg<D, NQ>::THREADS, NQ == 1 ? 2 : 1)
         }
       }
       if (valid) {
-        if (it.slot >= 0)
+        if (slot >= 0)
           p.ml[prow] = any ? make_float2(m_use, l_run) : make_float2(-INFINITY, 0.f);
         else if (p.lse)
           p.lse[(long long)head * p.Tq + tr] = any ? pack_lse(m_use, l_run) : -INFINITY;
@@ -693,21 +822,26 @@ __global__ void __launch_bounds__(PackCfg<D, NQ>::THREADS, NQ == 1 ? 2 : 1)
         float o[E], m, l;
         packed_exact_row<D>(p.q.p + s_head * p.q.sH + (long long)s_tr * p.q.sL, kb, p.k.sL, vb, p.v.sL, from, s_seen,
                             sc, o, m, l);
-        const long long s_prow = it.slot * R + (long long)s_tr * (p.Hkv * p.G) + s_head;
+        const long long s_prow = slot * R + (long long)s_tr * (p.Hkv * p.G) + s_head;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if (it.slot < 0)
+          if (slot < 0)
             p.o[s_head * p.osH + s_tr * p.osL + lane * E + e] = __float2bfloat16(o[e] / l);
           else
             p.part[s_prow * D + lane * E + e] = o[e];
         }
         if (lane == 0) {
-          if (it.slot >= 0)
+          if (slot >= 0)
             p.ml[s_prow] = make_float2(m, l);
           else if (p.lse)
             p.lse[(long long)s_head * p.Tq + s_tr] = pack_lse(m, l);
         }
       }
+      done_item(k);
+    }
+    if (!ok) {
+      abort_flag = 1;
+      report_error(-6);
     }
   }
   tc_fence_before();
@@ -739,13 +873,15 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
   }
   const PackSeq s = pack_seq(p, lo);
   if (tok < s.q0 || tok >= s.q0 + s.lq) return;
+  int rows = 0;
   if (p.Lp) {  // a malformed table may leave rows without their prefix part
     const PackSeq all = pack_all(p);
     if (tok < all.q0 || tok >= all.q0 + all.lq) return;
+    rows = all.lq;
   }
-  const int c = *p.chunk, t = pack_tiles(s.lk);
-  const int np = p.Lp ? pack_splits(pack_tiles(p.Lp), c, p.max_np) : 0;
-  const int ns = (p.Lp && t == 0) ? 0 : pack_splits(t, c, p.max_ns);
+  const int c = *p.chunk;
+  const int np = p.Lp ? pack_splits(pack_tiles(p.Lp), rows <= p.TQ, c, p.max_np) : 0;
+  const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
   if (!p.Lp && ns == 1) return;   // its item finished the row
   float m = -INFINITY;
   for (int i = lane; i < np + ns; i += 32) m = fmaxf(m, p.ml[i * R + row].x);

@@ -467,6 +467,10 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   p.TQ = pack_tokens(G);
   p.causal = causal != 0;
   p.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  // heads at a time: as many as keep K and V within half of the 126 MB L2, in even groups
+  const int64_t fit = std::max<int64_t>(1, ((int64_t)63 << 20) / (4 * (K->L + p.Lp) * Q->D));
+  const int64_t groups = (K->H + fit - 1) / fit;
+  p.group = (int)((K->H + groups - 1) / groups);
   p.q = view(Q);
   p.k = view(K);
   p.v = view(V);

@@ -28,11 +28,14 @@
 //
 // Roles: warps 0 .. 7 softmax (thread = row; warpgroup g is stream g); in the last
 // warpgroup one warp that takes items and loads, and one for the MMAs; each walks the
-// items by itself.  TMEM: S_g (128 fp32 columns, reused for P as 64 columns of bf16
-// pairs) and O_g (D fp32 columns).  The MMA warp's order per key tile j is PV_g(j),
-// S_g(j+1) for each g: S_g(j+1) may overwrite the columns of P_g(j) because the tensor
-// core runs a CTA's MMAs in order, and the commit of S_g(j+1) also says that PV_g(j)
-// is complete, so the softmax may rescale O_g without another barrier.
+// items by itself.  The softmax works on half tiles of 64 keys: with two buffers of 64
+// columns per stream, the scores of the next half are there when it is done with one
+// (whole tiles in one buffer left the tensor core 45 % idle: 480p 10.6 ms; the second buffer
+// costs shared-memory bandwidth, a 64-column MMA reading Q twice as often).  TMEM: S_g in
+// two buffers of 64 fp32 columns, each reused for P as 32 columns of bf16 pairs, and O_g (D
+// fp32 columns).  The MMA warp's order per half h is PV_g(h), S_g(h+2) for each g:
+// S_g(h+2) may overwrite the columns of P_g(h) because the tensor core runs a CTA's MMAs
+// in order.
 //
 // The running maximum moves only when it grows by more than 2^8 (a shift that
 // leaves the quotient unchanged: P stays below 256 and its bf16 rounding is
@@ -55,6 +58,7 @@
 namespace lx {
 
 constexpr int kPkKeys = 128;         // keys of a tile
+constexpr int kPkHalf = 64;          // keys of a softmax step
 constexpr int kPkSplitKeys = 2;      // a split covers at least this many tiles
 constexpr int kPkFine = 6;           // from this many tiles on, three splits for a CTA's share of the work
 constexpr int kPkSMs = 148;
@@ -68,15 +72,12 @@ struct PackCfg {
   static constexpr int RING = D == 128 ? 5 : 8;        // K and V tiles beside the two of Q
   static constexpr int OFF_RING = 2 * TILE_BYTES;
   static constexpr int SMEM = 1024 + OFF_RING + RING * TILE_BYTES;
-  static constexpr int READERS = 9;                    // warps that read an item: softmax, MMA
-  static constexpr int THREADS = 384;                  // softmax warpgroups; loads, MMA and two idle warps
-  // registers per thread: 168 at launch, then moved to the softmax, whose threads hold a
-  // row of 128 scores: 128 x 72 + 256 x 216 = 384 x 168
-  static constexpr int REGS_AUX = 72, REGS_SOFTMAX = 216;
-  static constexpr uint32_t S_COL = 0;                 // + 128 g
+  static constexpr int READERS = 10;                   // warps that read an item: softmax, MMA
+  static constexpr int THREADS = 384;                  // softmax warpgroups; loads, two MMA warps, one idle
+  static constexpr uint32_t S_COL = 0;                 // + 128 g + 64 b
   static constexpr uint32_t O_COL = 256;               // + D g
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t IDESC_S = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 0, 128, kPkKeys);
+  static constexpr uint32_t IDESC_S = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 0, 128, kPkHalf);
   static constexpr uint32_t IDESC_PV = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 1, 128, D);
 };
 
@@ -95,6 +96,7 @@ struct PackParams {
   float2* ml;            // [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
   int* chunk;            // tiles per split, for the combine kernel
   int max_np, max_ns;    // most splits of the prefix, of a sequence
+  int group;             // key/value heads worked on at a time
   unsigned long long limit_ns;
 };
 
@@ -148,6 +150,7 @@ struct PackItem {
   int t0, off;           // its index in the sequence; causal: token t sees keys <= t + off
   int k0, lk;            // first key row, keys
   int lo[2], nt[2];      // first key tile and number of key tiles of each stream
+  int nh[2];             // number of halves with a key that some row sees
   int slot[2];           // where a stream's partial result goes; -1: it finishes its rows; -2: no rows
   int head;              // key/value head
   int prefix;            // keys of the prefix (no causal rule)
@@ -246,16 +249,19 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   __syncthreads();
 }
 
-// Item number `id` (a warp together); stop past the last one.  A head's items follow
-// one another: the prefix, then the last rows of the last sequence first (with the
-// causal rule the long items start first).
+// Item number `id` (a warp together); stop past the last one.  In the order of a head's
+// items the prefix comes first, then the last rows of the last sequence (with the causal
+// rule the long items start first); p.group heads, whose K and V fit the L2 cache
+// together, take turns in it.
 __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& tb, int id, PackItem& it) {
   const int lane = threadIdx.x & 31;
   it.stop = 1;
   if (id / p.Hkv >= tb.total) return;   // total * Hkv items in all
   it.stop = 0;
-  it.head = id / tb.total;
-  int x = id % tb.total;
+  const int first_head = id / (tb.total * p.group) * p.group, heads = min(p.group, p.Hkv - first_head);
+  id -= first_head * tb.total;
+  it.head = first_head + id % heads;
+  int x = id / heads;
   PackSeq s{0, 0, 0, 0};
   int ns, base = -1;                    // splits; slot of the first one
   it.prefix = x < tb.pi;
@@ -310,11 +316,13 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
     const int sp = it.narrow ? 2 * x + g : x % ns, first = it.narrow ? 0 : g * p.TQ;
     const int tokens = min(p.TQ, it.q_end - it.q0 - first);
     int lo = min(sp * per, T), hi = min(lo + per, T);
-    // key tiles up to the last key that the tile's last token sees
-    if (p.causal && !it.prefix) hi = min(hi, pack_tiles(max(0, min(s.lk, it.t0 + first + tokens + it.off))));
+    // keys up to the last one that the tile's last token sees
+    int keys = min(s.lk, hi * kPkKeys);
+    if (p.causal && !it.prefix) keys = min(keys, it.t0 + first + tokens + it.off);
     const bool live = tokens > 0 && sp < ns;
     it.lo[g] = lo;
-    it.nt[g] = live ? max(0, hi - lo) : 0;
+    it.nh[g] = live ? pack_div(max(0, keys - lo * kPkKeys), kPkHalf) : 0;
+    it.nt[g] = (it.nh[g] + 1) / 2;
     it.slot[g] = !live ? -2 : (base < 0 ? -1 : base + sp);
   }
 }
@@ -338,6 +346,24 @@ __device__ __forceinline__ int clc_answer(const void* answer) {
       : "r"(smem_u32(answer))
       : "memory");
   return ok ? (int)x : -1;
+}
+
+// ---------------------------------------------------------------- MMA issue
+// One thread issues every MMA of a stream, so the instructions per MMA count: operands
+// are the low words of their descriptors (the high word is common).
+__device__ __forceinline__ void mma_f16_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};"
+      "\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};"
+      "\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
 }
 
 // One row over keys [lo, hi), a warp together: lane holds D / 32 neighbouring
@@ -383,10 +409,10 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   constexpr int NQ = 2;   // streams
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // full/empty: a ring slot; qfull/qempty[g]: the tile Q_g; sfull[g]: S_g complete; pfull[g]: P_g written;
-  // odone[g]: O_g complete; ifull/iempty: an item slot; clc: an answer of the launch control
-  __shared__ uint64_t bar_full[C::RING], bar_empty[C::RING], bar_qfull[NQ], bar_qempty[NQ], bar_sfull[NQ], bar_pfull[NQ],
-      bar_odone[NQ], bar_ifull[kPkItems], bar_iempty[kPkItems], bar_clc, bar_drain;
+  // full/empty: a ring slot; qfull/qempty[g]: the tile Q_g; per buffer b: sfull[g][b]: S complete, pfull[g][b]: P
+  // written, pvdone[g][b]: P V complete; ifull/iempty: an item slot; clc: an answer of the launch control
+  __shared__ uint64_t bar_full[C::RING], bar_empty[C::RING], bar_qfull[NQ], bar_qempty[NQ], bar_sfull[NQ][2],
+      bar_pfull[NQ][2], bar_pvdone[NQ][2], bar_ifull[kPkItems], bar_iempty[kPkItems], bar_clc, bar_drain[NQ];
   __shared__ __align__(16) uint4 clc;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -402,21 +428,23 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::RING; ++s) {
       mbar_init(&bar_full[s], 1);
-      mbar_init(&bar_empty[s], 1);
+      mbar_init(&bar_empty[s], 2);   // both streams
     }
     for (int g = 0; g < NQ; ++g) {
       mbar_init(&bar_qfull[g], 1);
       mbar_init(&bar_qempty[g], 1);
-      mbar_init(&bar_sfull[g], 1);
-      mbar_init(&bar_pfull[g], 4);  // one arrival per softmax warp
-      mbar_init(&bar_odone[g], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bar_sfull[g][b], 1);
+        mbar_init(&bar_pfull[g][b], 4);  // one arrival per softmax warp
+        mbar_init(&bar_pvdone[g][b], 1);
+      }
     }
     for (int s = 0; s < kPkItems; ++s) {
       mbar_init(&bar_ifull[s], 1);
       mbar_init(&bar_iempty[s], C::READERS);
     }
     mbar_init(&bar_clc, 1);
-    mbar_init(&bar_drain, 1);
+    for (int g = 0; g < NQ; ++g) mbar_init(&bar_drain[g], 1);
     abort_flag = 0;
     never_abort = 0;
     fence_barrier_init();
@@ -439,7 +467,6 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     if (lane == 0) mbar_arrive(&bar_iempty[k % kPkItems]);
   };
   if (warp >= 4 * NQ) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
     if (warp == TMA_WARP) {
       // ================= items and loads: Q, then K(0), V(0), K(1), V(1), ... =================
       const bool leader = elect_one();
@@ -541,111 +568,127 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           mbar_wait(&bar_full[j % C::RING], (uint32_t)(j / C::RING) & 1u, &never_abort, p.limit_ns);
       }
       __syncwarp();
-    } else if (warp == MMA_WARP) {
-      // ================= MMA: per key tile j and row tile g, O_g += P_g(j) V(j), then S_g(j+1) =================
-      const uint32_t sbase = smem_u32(sm);
-      const bool leader = elect_one();
+      } else if (warp >= MMA_WARP && warp < MMA_WARP + 2) {
+      // ================= MMA of stream g: per half h, O += P(h) V(h), then S(h+2) =================
+      const int g = warp - MMA_WARP;
+      const uint32_t sbase = smem_u32(sm), scol = tbase + C::S_COL + 128 * g, ocol = tbase + C::O_COL + D * g;
+      // descriptors: the high word is the same for all, the low word holds address and leading offset
+      const uint64_t dkm = smem_desc(sbase + C::OFF_RING, 16, 1024, SW_128B);
+      const uint32_t hi = (uint32_t)(dkm >> 32), ring_k = (uint32_t)dkm;
+      const uint32_t ring_v = (uint32_t)smem_desc(sbase + C::OFF_RING, 128 * 128, 1024, SW_128B);
+      const uint32_t dq = (uint32_t)smem_desc(sbase + g * C::TILE_BYTES, 16, 1024, SW_128B);
       bool ok = true;
-      int m = 0;                 // ring position of this item's first load
-      int uq[NQ], up[NQ];        // Q tiles and P tiles used
-#pragma unroll
-      for (int g = 0; g < NQ; ++g) uq[g] = 0, up[g] = 0;
-      auto wait_full = [&](int at) {
+      int m = 0, uq = 0, u = 0;  // ring position of this item's first load; Q tiles used; halves done before this item
+      // Both streams walk all loads in order and both free each slot: a stream that only
+      // waited for its own tiles could be a turn of the ring ahead or behind on a
+      // slot, which a phase's parity does not show.
+      int seen = 0;
+      auto wait_load = [&](int at) {
         return warp_wait(&bar_full[at % C::RING], (uint32_t)(at / C::RING) & 1u, &abort_flag, p.limit_ns);
       };
-      // S_g = Q_g K^T; the K tile is free after its last reader, Q_g after the item's last tile
-      auto issue_s = [&](int g, int at, bool free_k, bool free_q) {
-        const int slot = at % C::RING;
-        const uint64_t dq = smem_desc(sbase + g * C::TILE_BYTES, 16, 1024, SW_128B);
-        const uint64_t dk = smem_desc(sbase + C::OFF_RING + slot * C::TILE_BYTES, 16, 1024, SW_128B);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t step = (uint64_t)(((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4);
-          mma_ss<KIND_F16>(tbase + C::S_COL + 128 * g, dq + step, dk + step, C::IDESC_S, kk > 0 ? 1u : 0u);
+      auto skip_to = [&](int at) {   // loads of the other stream: nothing to do with them
+        for (; seen < at; ++seen) {
+          if (!wait_load(seen)) return false;
+          if (lane == 0) mbar_arrive(&bar_empty[seen % C::RING]);
         }
-        mma_commit(&bar_sfull[g]);
-        if (free_k) mma_commit(&bar_empty[slot]);
-        if (free_q) mma_commit(&bar_qempty[g]);
+        return true;
+      };
+      auto wait_full = [&](int at) {
+        if (!skip_to(at) || !wait_load(at)) return false;
+        seen = at + 1;
+        return true;
       };
       for (int k = 0; ok; ++k) {
         ok = next_item(k);
         if (!ok) break;
         const PackItem& it = items[k % kPkItems];
-        const int n0 = it.nt[0], n1 = it.nt[1], most = max(n0, n1);
+        const int t0 = it.nt[0], t1 = it.nt[1], n = it.nh[g];
         const bool stop = it.stop, narrow = it.narrow;
-        const int keys0 = it.lk - it.lo[0] * kPkKeys, keys1 = it.lk - it.lo[1] * kPkKeys;   // from the first tile on
+        const int keys = it.lk - it.lo[g] * kPkKeys;   // from the first tile on
         done_item(k);
         if (stop) break;
-        if (most == 0) continue;
-        // ring position of K_g(j) and V_g(j); narrow: n0 >= n1, four loads a step while both run
-        auto at_k = [&](int g, int j) {
-          return narrow ? m + (j < n1 ? 4 * j + g : 2 * (j + n1)) : m + 2 * j;
-        };
-        auto at_v = [&](int g, int j) {
-          return narrow ? m + (j < n1 ? 4 * j + 2 + g : 2 * (j + n1) + 1) : m + 2 * j + 1;
-        };
-        // the last stream that reads a tile of step j frees it
-        auto frees = [&](int g, int j) { return narrow || g == (n1 > j ? 1 : 0); };
-#pragma unroll
-        for (int g = 0; g < NQ; ++g) {
-          if (!ok || (g ? n1 : n0) == 0) continue;
-          ok = wait_full(at_k(g, 0)) && warp_wait(&bar_qfull[g], (uint32_t)(uq[g]++) & 1u, &abort_flag, p.limit_ns);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) issue_s(g, at_k(g, 0), frees(g, 0), (g ? n1 : n0) == 1);
-          __syncwarp();
+        // ring position of K(j) and V(j); narrow: t0 >= t1, four loads a step while both streams run
+        int at = m + (narrow ? g : 0);
+        m += narrow ? 2 * (t0 + t1) : 2 * max(t0, t1);
+        if (n == 0) {
+          ok = skip_to(m);
+          continue;
         }
-        for (int j = 0; ok && j < most; ++j) {
+        ok = wait_full(at) && warp_wait(&bar_qfull[g], (uint32_t)(uq++) & 1u, &abort_flag, p.limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        auto issue_s = [&](int h, int slot) {   // S(h) = Q K(h)^T
+          const uint32_t b = (u + h) & 1, dk = ring_k + slot * (C::TILE_BYTES >> 4) + (h & 1) * (64 * 128 >> 4);
 #pragma unroll
-          for (int g = 0; g < NQ; ++g) {
-            const int n = g ? n1 : n0;
-            if (!ok || j >= n) continue;
-            const int va = at_v(g, j), vslot = va % C::RING;
-            ok = wait_full(va);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t step = ((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4;
+            mma_f16_lo(scol + 64 * b, dq + step, dk + step, hi, C::IDESC_S, kk > 0);
+          }
+          mma_commit(&bar_sfull[g][b]);
+          if ((h & 1) || h + 1 == n) mma_commit(&bar_empty[slot]);
+          if (h + 1 == n) mma_commit(&bar_qempty[g]);
+        };
+        int kslot = at % C::RING;
+        if (elect_one()) {
+          issue_s(0, kslot);
+          if (n > 1) issue_s(1, kslot);
+        }
+        __syncwarp();
+        for (int h = 0; h < n; ++h) {
+          const int b = (u + h) & 1, j = h >> 1;
+          // V of this tile, and K of the next
+          const int va = narrow ? at + (j < t1 ? 2 : 1) : at + 1, vslot = va % C::RING;
+          if (!(h & 1)) {
+            const int next = narrow ? (j + 1 < t1 ? at + 4 : (j < t1 ? at + 4 - g : at + 2)) : at + 2;
+            ok = wait_full(va) && (h + 2 >= n || wait_full(next));
             if (!ok) break;
+            kslot = next % C::RING;
             // V rows past the sequence's end belong to somebody else: zero them
-            const int left = (g ? keys1 : keys0) - j * kPkKeys;
-            if (left < kPkKeys && (g == 0 || narrow || n0 <= j)) {
+            const int left = keys - j * kPkKeys;
+            if (left < kPkKeys) {
               uint8_t* vt = sm + C::OFF_RING + vslot * C::TILE_BYTES;
               for (int a = 0; a < C::NATOM; ++a)
-                for (int b = left * 128 + lane * 16; b < kPkKeys * 128; b += 512)
-                  *reinterpret_cast<uint4*>(vt + a * 128 * 128 + b) = make_uint4(0, 0, 0, 0);
+                for (int y = left * 128 + lane * 16; y < kPkKeys * 128; y += 512)
+                  *reinterpret_cast<uint4*>(vt + a * 128 * 128 + y) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
               __syncwarp();
             }
-            ok = warp_wait(&bar_pfull[g], (uint32_t)(up[g]++) & 1u, &abort_flag, p.limit_ns) &&
-                 (j + 1 >= n || wait_full(at_k(g, j + 1)));
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-              const uint64_t dv = smem_desc(sbase + C::OFF_RING + vslot * C::TILE_BYTES, 128 * 128, 1024, SW_128B);
-#pragma unroll
-              for (int kk = 0; kk < kPkKeys / 16; ++kk)
-                mma_ts<KIND_F16>(tbase + C::O_COL + D * g, tbase + C::S_COL + 128 * g + 8 * kk,
-                                 dv + (uint64_t)((kk * 16 * 128) >> 4), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-              if (j + 1 == n) mma_commit(&bar_odone[g]);
-              if (frees(g, j)) mma_commit(&bar_empty[vslot]);
-              if (j + 1 < n) issue_s(g, at_k(g, j + 1), frees(g, j + 1), j + 2 == n);
-            }
-            __syncwarp();
           }
+          ok = warp_wait(&bar_pfull[g][b], (uint32_t)((u + h) >> 1) & 1u, &abort_flag, p.limit_ns);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t dv = ring_v + vslot * (C::TILE_BYTES >> 4) + (h & 1) * (64 * 128 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kPkHalf / 16; ++kk) {
+              if (kk == 0)
+                mma_f16_ts_lo(ocol, scol + 64 * b, dv, hi, C::IDESC_PV, h > 0);
+              else
+                mma_f16_ts_lo(ocol, scol + 64 * b + 8 * kk, dv + (uint32_t)((kk * 16 * 128) >> 4), hi, C::IDESC_PV, true);
+            }
+            mma_commit(&bar_pvdone[g][b]);
+            if ((h & 1) || h + 1 == n) mma_commit(&bar_empty[vslot]);
+            if (h + 2 < n) issue_s(h + 2, kslot);
+          }
+          __syncwarp();
+          if (h & 1) at = narrow ? (j + 1 < t1 ? at + 4 : (j < t1 ? at + 4 - g : at + 2)) : at + 2;
         }
-        m += narrow ? 2 * (n0 + n1) : 2 * most;
+        u += n;
+        ok = ok && skip_to(m);
       }
-      if (leader) {
+      if (elect_one()) {
         if (!ok) {
           abort_flag = 1;
           report_error(-6);
         }
         // drain: every issued MMA completes before TMEM is released
-        mma_commit(&bar_drain);
-        mbar_wait(&bar_drain, 0, &never_abort, p.limit_ns);
+        mma_commit(&bar_drain[g]);
+        mbar_wait(&bar_drain[g], 0, &never_abort, p.limit_ns);
       }
       __syncwarp();
     }
   } else {
     // ================= softmax, rescale, epilogue: thread = row =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     const int g = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const int row_tok = row / p.G, row_head = row % p.G;
@@ -653,7 +696,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_addr = tbase + lanes + C::S_COL + 128 * g, o_addr = tbase + lanes + C::O_COL + D * g;
     const float sc = p.scale_log2;
-    int us = 0, uo = 0;        // S tiles and O tiles read
+    int u = 0;                 // halves done: buffer u & 1, its barriers' phase u >> 1
     bool ok = true;
     for (int k = 0; ok; ++k) {
       ok = next_item(k);
@@ -665,33 +708,37 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       const bool warp_live = __any_sync(0xffffffffu, valid);
       // keys [0, seen) of the sequence are visible to this row
       const int seen = (p.causal && !it.prefix) ? max(0, min(it.lk, it.t0 + tok + it.off + 1)) : it.lk;
-      const int my_nt = it.nt[g], lo = it.lo[g], ahead = seen - lo * kPkKeys;
+      const int my_nh = it.nh[g], lo = it.lo[g], ahead = seen - lo * kPkKeys;
       float m_use = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < my_nt; ++j) {
-        ok = warp_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, p.limit_ns);
+      for (int h = 0; h < my_nh; ++h, ++u) {
+        const int b = u & 1;
+        const uint32_t sb = s_addr + 64 * b;
+        ok = warp_wait(&bar_sfull[g][b], (uint32_t)(u >> 1) & 1u, &abort_flag, p.limit_ns);
         if (!ok) break;
         tc_fence_after();
         if (warp_live) {
-          uint32_t sv[128];
-  #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+          uint32_t sv[64];
+          uint32_t (&s_lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[0]);
+          uint32_t (&s_hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[32]);
+          tmem_ld32(sb, s_lo);
+          tmem_ld32(sb + 32, s_hi);
           tmem_wait_ld();
-  #pragma unroll
-          for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-          const int nv = ahead - j * kPkKeys;               // visible columns of this tile
-          if (__any_sync(0xffffffffu, nv < kPkKeys)) {
-  #pragma unroll
-            for (int u = 0; u < 128; ++u)
-              if (u >= nv) sv[u] = 0xFF800000u;             // -inf
+          reg_fence32(s_lo);
+          reg_fence32(s_hi);
+          const int nv = ahead - h * kPkHalf;               // visible columns of this half
+          if (__any_sync(0xffffffffu, nv < kPkHalf)) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= nv) sv[c] = 0xFF800000u;             // -inf
           }
           const float* f = reinterpret_cast<const float*>(sv);
           float t8[8];
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float a = fmaxf(f[i], f[i + 8]);
-  #pragma unroll
-            for (int u = 16; u < 112; u += 16) a = fmax3(a, f[i + u], f[i + u + 8]);
-            t8[i] = fmax3(a, f[i + 112], f[i + 120]);
+            float a = fmax3(f[i], f[i + 8], f[i + 16]);
+            a = fmax3(a, f[i + 24], f[i + 32]);
+            a = fmax3(a, f[i + 40], f[i + 48]);
+            t8[i] = fmaxf(a, f[i + 56]);
           }
           const float mx = fmaxf(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], fmax3(t8[5], t8[6], t8[7]))) * sc;
           const bool grow = mx > m_use + kPkLazy;           // also the first finite maximum
@@ -699,15 +746,19 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
             const float alpha = grow ? ex2f(m_use - mx) : 1.f;   // 0 from -inf
             if (grow) m_use = mx;
             l_run *= alpha;
-            if (j > 0) {
+            if (h > 0) {
+              // the product of the half before must be in O
+              ok = warp_wait(&bar_pvdone[g][b ^ 1], (uint32_t)((u - 1) >> 1) & 1u, &abort_flag, p.limit_ns);
+              if (!ok) break;
+              tc_fence_after();
               const uint64_t a2 = f2pack(alpha, alpha);
-  #pragma unroll 1
+#pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_addr + c, o);
                 tmem_wait_ld();
                 reg_fence32(o);
-  #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                   float x, y;
                   f2unpack(mul2(f2pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x, y);
@@ -721,18 +772,17 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           const float at = m_use == -INFINITY ? 0.f : m_use;  // nothing visible yet: exp2(-inf - 0) = 0
           const uint64_t sc2 = f2pack(sc, sc), nm2 = f2pack(-at, -at);
           uint64_t sum2[4] = {0, 0, 0, 0};
-          uint32_t pk[64];
-  #pragma unroll
-          for (int u = 0; u < 128; u += 2) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
             float x0, x1;
-            f2unpack(fma2(f2pack(__uint_as_float(sv[u]), __uint_as_float(sv[u + 1])), sc2, nm2), x0, x1);
+            f2unpack(fma2(f2pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, nm2), x0, x1);
             const float p0 = ex2f(x0), p1 = ex2f(x1);
-            sum2[(u >> 1) & 3] = add2(sum2[(u >> 1) & 3], f2pack(p0, p1));
+            sum2[(c >> 1) & 3] = add2(sum2[(c >> 1) & 3], f2pack(p0, p1));
             const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
-            pk[u >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
+            pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
           }
-          tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-          tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          tmem_st32(sb, pk);
           float a0, a1, b0, b1;
           f2unpack(add2(sum2[0], sum2[1]), a0, a1);
           f2unpack(add2(sum2[2], sum2[3]), b0, b1);
@@ -741,10 +791,10 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_pfull[g]);
+        if (lane == 0) mbar_arrive(&bar_pfull[g][b]);
       }
-      if (ok && my_nt > 0) {
-        ok = warp_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, p.limit_ns);
+      if (ok && my_nh > 0) {
+        ok = warp_wait(&bar_pvdone[g][(u - 1) & 1], (uint32_t)((u - 1) >> 1) & 1u, &abort_flag, p.limit_ns);
         tc_fence_after();
       }
       if (!ok) break;
@@ -754,8 +804,8 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       }
       const int head = it.head * p.G + row_head;
       const int from = lo * kPkKeys;                          // keys [from, to) were computed
-      const int to = min(it.lk, (lo + my_nt) * kPkKeys);
-      const bool any = valid && seen > from && my_nt > 0;        // this row saw a key
+      const int to = min(it.lk, from + my_nh * kPkHalf);
+      const bool any = valid && seen > from && my_nh > 0;        // this row saw a key
       const float inv = slot < 0 ? 1.0f / l_run : 1.0f;
       const long long tr = it.q0 + tok;
       __nv_bfloat16* orow = p.o + head * p.osH + tr * p.osL;
@@ -765,7 +815,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
-        if (my_nt > 0) {
+        if (my_nh > 0) {
           tmem_ld32(o_addr + c, o);
           tmem_wait_ld();
           reg_fence32(o);

@@ -27,20 +27,25 @@
 // end of the one before it.
 //
 // Roles: warps 0 .. 7 softmax (thread = row; warpgroup g is stream g); in the last
-// warpgroup one warp that takes items and loads, and one for the MMAs; each walks the
-// items by itself.  The softmax works on half tiles of 64 keys: with two buffers of 64
-// columns per stream, the scores of the next half are there when it is done with one
-// (whole tiles in one buffer left the tensor core 45 % idle: 480p 10.6 ms; the second buffer
-// costs shared-memory bandwidth, a 64-column MMA reading Q twice as often).  TMEM: S_g in
-// two buffers of 64 fp32 columns, each reused for P as 32 columns of bf16 pairs, and O_g (D
-// fp32 columns).  The MMA warp's order per half h is PV_g(h), S_g(h+2) for each g:
-// S_g(h+2) may overwrite the columns of P_g(h) because the tensor core runs a CTA's MMAs
-// in order.
+// warpgroup one warp that takes items and loads, and an MMA warp for each stream; each
+// walks the items by itself.  TMEM: S_g (128 fp32 columns; P of the first and of the
+// second half of the keys, 32 columns of bf16 pairs each, takes the place of the half's
+// first columns) and O_g (D fp32 columns).  A stream's order per key tile j is the product
+// of the first half of P(j) with V, that of the second half, S(j+1): the first product
+// runs under the second half's exponentials, S(j+1) may overwrite P(j) because the tensor
+// core runs a thread's MMAs in order, and its commit also says that O has P(j) V(j), so
+// the softmax may rescale O without another barrier.  (Half tiles with two score
+// buffers, which take the scores out of the stream's chain, were slower: 12.1 against
+// 10.4 ms for the 480p grid, a 64-column MMA reading Q twice as often and every half paying
+// for its own hand-over.)
 //
-// The running maximum moves only when it grows by more than 2^8 (a shift that
-// leaves the quotient unchanged: P stays below 256 and its bf16 rounding is
-// relative), so O is rarely rescaled.  P is rounded to bf16, the type of V and
-// of the output; the row sum takes the unrounded fp32 values.
+// The reference that the exponents are taken against is not the running maximum but
+// follows it: it moves when the maximum has passed it by more than 2^8, and the maximum
+// of a tile counts from the next tile on, so that the exponentials do not wait for it (a
+// shift leaves the quotient unchanged: P's rounding to bf16 is relative, and a tile
+// whose scores pass the reference by 2^16 gets a new one at once).  O is
+// rarely rescaled.  P is rounded to bf16, the type of V and of the output; the row sum
+// takes the unrounded fp32 values.
 //
 // Values in masked places: scores are replaced by -inf by selection, and V rows
 // past a sequence's end are zeroed in shared memory before they are used.  A
@@ -58,12 +63,13 @@
 namespace lx {
 
 constexpr int kPkKeys = 128;         // keys of a tile
-constexpr int kPkHalf = 64;          // keys of a softmax step
+constexpr int kPkHalf = 64;          // keys of a product with V
 constexpr int kPkSplitKeys = 2;      // a split covers at least this many tiles
 constexpr int kPkFine = 6;           // from this many tiles on, three splits for a CTA's share of the work
 constexpr int kPkSMs = 148;
 constexpr int kPkItems = 4;          // items published ahead of their last reader
-constexpr float kPkLazy = 8.0f;      // log2 growth of the row maximum that forces a rescale
+constexpr float kPkLazy = 8.0f;      // log2 growth of the row maximum that moves the reference
+constexpr float kPkFar = 16.0f;      // log2 distance from the reference that a tile may have
 
 template <int D>
 struct PackCfg {
@@ -74,10 +80,13 @@ struct PackCfg {
   static constexpr int SMEM = 1024 + OFF_RING + RING * TILE_BYTES;
   static constexpr int READERS = 10;                   // warps that read an item: softmax, MMA
   static constexpr int THREADS = 384;                  // softmax warpgroups; loads, two MMA warps, one idle
-  static constexpr uint32_t S_COL = 0;                 // + 128 g + 64 b
+  // registers per thread: 168 at launch, then moved to the softmax, whose threads hold a
+  // half row of scores and of P: 128 x 72 + 256 x 216 = 384 x 168
+  static constexpr int REGS_AUX = 72, REGS_SOFTMAX = 216;
+  static constexpr uint32_t S_COL = 0;                 // + 128 g
   static constexpr uint32_t O_COL = 256;               // + D g
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t IDESC_S = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 0, 128, kPkHalf);
+  static constexpr uint32_t IDESC_S = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 0, 128, kPkKeys);
   static constexpr uint32_t IDESC_PV = instr_desc(IDESC_DF32, IDESC_BF16, IDESC_BF16, 0, 1, 128, D);
 };
 
@@ -366,6 +375,22 @@ __device__ __forceinline__ void mma_f16_ts_lo(uint32_t d, uint32_t a, uint32_t b
       : "memory");
 }
 
+// 4 x 4 transposition of 16-byte pieces within each four lanes: lane i gives piece w
+// of its own and gets piece i of lane w's.
+__device__ __forceinline__ void transpose4(uint4 (&h)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto swap = [&](uint4& a, uint4& b, int mask, bool up) {   // lanes with `up` give a and get b's place
+    const uint4 g = up ? a : b;
+    const uint4 r = make_uint4(__shfl_xor_sync(0xffffffffu, g.x, mask), __shfl_xor_sync(0xffffffffu, g.y, mask),
+                               __shfl_xor_sync(0xffffffffu, g.z, mask), __shfl_xor_sync(0xffffffffu, g.w, mask));
+    if (up) a = r; else b = r;
+  };
+  swap(h[0], h[1], 1, lane & 1);
+  swap(h[2], h[3], 1, lane & 1);
+  swap(h[0], h[2], 2, lane & 2);
+  swap(h[1], h[3], 2, lane & 2);
+}
+
 // One row over keys [lo, hi), a warp together: lane holds D / 32 neighbouring
 // channels.  Returns the unnormalised row, its maximum (log2 domain) and sum.
 template <int D>
@@ -409,10 +434,10 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   constexpr int NQ = 2;   // streams
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // full/empty: a ring slot; qfull/qempty[g]: the tile Q_g; per buffer b: sfull[g][b]: S complete, pfull[g][b]: P
-  // written, pvdone[g][b]: P V complete; ifull/iempty: an item slot; clc: an answer of the launch control
-  __shared__ uint64_t bar_full[C::RING], bar_empty[C::RING], bar_qfull[NQ], bar_qempty[NQ], bar_sfull[NQ][2],
-      bar_pfull[NQ][2], bar_pvdone[NQ][2], bar_ifull[kPkItems], bar_iempty[kPkItems], bar_clc, bar_drain[NQ];
+  // full/empty: a ring slot; qfull/qempty[g]: the tile Q_g; sfull[g]: S complete; pfull[g][b]: half b of P
+  // written; odone[g]: O complete; ifull/iempty: an item slot; clc: an answer of the launch control
+  __shared__ uint64_t bar_full[C::RING], bar_empty[C::RING], bar_qfull[NQ], bar_qempty[NQ], bar_sfull[NQ],
+      bar_pfull[NQ][2], bar_odone[NQ], bar_ifull[kPkItems], bar_iempty[kPkItems], bar_clc, bar_drain[NQ];
   __shared__ __align__(16) uint4 clc;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -433,11 +458,9 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     for (int g = 0; g < NQ; ++g) {
       mbar_init(&bar_qfull[g], 1);
       mbar_init(&bar_qempty[g], 1);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&bar_sfull[g][b], 1);
-        mbar_init(&bar_pfull[g][b], 4);  // one arrival per softmax warp
-        mbar_init(&bar_pvdone[g][b], 1);
-      }
+      mbar_init(&bar_sfull[g], 1);
+      for (int b = 0; b < 2; ++b) mbar_init(&bar_pfull[g][b], 4);  // one arrival per softmax warp
+      mbar_init(&bar_odone[g], 1);
     }
     for (int s = 0; s < kPkItems; ++s) {
       mbar_init(&bar_ifull[s], 1);
@@ -467,6 +490,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     if (lane == 0) mbar_arrive(&bar_iempty[k % kPkItems]);
   };
   if (warp >= 4 * NQ) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
     if (warp == TMA_WARP) {
       // ================= items and loads: Q, then K(0), V(0), K(1), V(1), ... =================
       const bool leader = elect_one();
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       }
       __syncwarp();
       } else if (warp >= MMA_WARP && warp < MMA_WARP + 2) {
-      // ================= MMA of stream g: per half h, O += P(h) V(h), then S(h+2) =================
+      // ================= MMA of stream g: per tile j, O += P(j) V(j) in two halves, then S(j+1) =================
       const int g = warp - MMA_WARP;
       const uint32_t sbase = smem_u32(sm), scol = tbase + C::S_COL + 128 * g, ocol = tbase + C::O_COL + D * g;
       // descriptors: the high word is the same for all, the low word holds address and leading offset
@@ -578,7 +602,8 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       const uint32_t ring_v = (uint32_t)smem_desc(sbase + C::OFF_RING, 128 * 128, 1024, SW_128B);
       const uint32_t dq = (uint32_t)smem_desc(sbase + g * C::TILE_BYTES, 16, 1024, SW_128B);
       bool ok = true;
-      int m = 0, uq = 0, u = 0;  // ring position of this item's first load; Q tiles used; halves done before this item
+      int m = 0, uq = 0;         // ring position of this item's first load; Q tiles used
+      int up[2] = {0, 0};        // halves of P used
       // Both streams walk all loads in order and both free each slot: a stream that only
       // waited for its own tiles could be a turn of the ring ahead or behind on a
       // slot, which a phase's parity does not show.
@@ -617,63 +642,60 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         ok = wait_full(at) && warp_wait(&bar_qfull[g], (uint32_t)(uq++) & 1u, &abort_flag, p.limit_ns);
         if (!ok) break;
         tc_fence_after();
-        auto issue_s = [&](int h, int slot) {   // S(h) = Q K(h)^T
-          const uint32_t b = (u + h) & 1, dk = ring_k + slot * (C::TILE_BYTES >> 4) + (h & 1) * (64 * 128 >> 4);
+        const int nt = (n + 1) / 2;
+        auto issue_s = [&](int slot, bool last) {   // S(j) = Q K(j)^T
+          const uint32_t dk = ring_k + slot * (C::TILE_BYTES >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t step = ((kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4;
-            mma_f16_lo(scol + 64 * b, dq + step, dk + step, hi, C::IDESC_S, kk > 0);
+            mma_f16_lo(scol, dq + step, dk + step, hi, C::IDESC_S, kk > 0);
           }
-          mma_commit(&bar_sfull[g][b]);
-          if ((h & 1) || h + 1 == n) mma_commit(&bar_empty[slot]);
-          if (h + 1 == n) mma_commit(&bar_qempty[g]);
+          mma_commit(&bar_sfull[g]);
+          mma_commit(&bar_empty[slot]);
+          if (last) mma_commit(&bar_qempty[g]);
         };
-        int kslot = at % C::RING;
-        if (elect_one()) {
-          issue_s(0, kslot);
-          if (n > 1) issue_s(1, kslot);
-        }
+        if (elect_one()) issue_s(at % C::RING, nt == 1);
         __syncwarp();
-        for (int h = 0; h < n; ++h) {
-          const int b = (u + h) & 1, j = h >> 1;
+        for (int j = 0; j < nt; ++j) {
           // V of this tile, and K of the next
           const int va = narrow ? at + (j < t1 ? 2 : 1) : at + 1, vslot = va % C::RING;
-          if (!(h & 1)) {
-            const int next = narrow ? (j + 1 < t1 ? at + 4 : (j < t1 ? at + 4 - g : at + 2)) : at + 2;
-            ok = wait_full(va) && (h + 2 >= n || wait_full(next));
-            if (!ok) break;
-            kslot = next % C::RING;
-            // V rows past the sequence's end belong to somebody else: zero them
-            const int left = keys - j * kPkKeys;
-            if (left < kPkKeys) {
-              uint8_t* vt = sm + C::OFF_RING + vslot * C::TILE_BYTES;
-              for (int a = 0; a < C::NATOM; ++a)
-                for (int y = left * 128 + lane * 16; y < kPkKeys * 128; y += 512)
-                  *reinterpret_cast<uint4*>(vt + a * 128 * 128 + y) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          ok = warp_wait(&bar_pfull[g][b], (uint32_t)((u + h) >> 1) & 1u, &abort_flag, p.limit_ns);
+          at = narrow ? (j + 1 < t1 ? at + 4 : (j < t1 ? at + 4 - g : at + 2)) : at + 2;
+          ok = wait_full(va) && (j + 1 >= nt || wait_full(at));
           if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t dv = ring_v + vslot * (C::TILE_BYTES >> 4) + (h & 1) * (64 * 128 >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kPkHalf / 16; ++kk) {
-              if (kk == 0)
-                mma_f16_ts_lo(ocol, scol + 64 * b, dv, hi, C::IDESC_PV, h > 0);
-              else
-                mma_f16_ts_lo(ocol, scol + 64 * b + 8 * kk, dv + (uint32_t)((kk * 16 * 128) >> 4), hi, C::IDESC_PV, true);
-            }
-            mma_commit(&bar_pvdone[g][b]);
-            if ((h & 1) || h + 1 == n) mma_commit(&bar_empty[vslot]);
-            if (h + 2 < n) issue_s(h + 2, kslot);
+          // V rows past the sequence's end belong to somebody else: zero them
+          const int left = keys - j * kPkKeys;
+          if (left < kPkKeys) {
+            uint8_t* vt = sm + C::OFF_RING + vslot * C::TILE_BYTES;
+            for (int a = 0; a < C::NATOM; ++a)
+              for (int y = left * 128 + lane * 16; y < kPkKeys * 128; y += 512)
+                *reinterpret_cast<uint4*>(vt + a * 128 * 128 + y) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          __syncwarp();
-          if (h & 1) at = narrow ? (j + 1 < t1 ? at + 4 : (j < t1 ? at + 4 - g : at + 2)) : at + 2;
+          const uint32_t dv = ring_v + vslot * (C::TILE_BYTES >> 4);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (b && 2 * j + 1 >= n) break;        // no visible key in the second half
+            ok = warp_wait(&bar_pfull[g][b], (uint32_t)(up[b]++) & 1u, &abort_flag, p.limit_ns);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kPkHalf / 16; ++kk)
+                mma_f16_ts_lo(ocol, scol + 64 * b + 8 * kk, dv + (uint32_t)(((64 * b + kk * 16) * 128) >> 4), hi,
+                              C::IDESC_PV, b || kk || j > 0);
+              if (2 * j + b + 1 == n || b) {
+                mma_commit(&bar_empty[vslot]);
+                if (j + 1 == nt)
+                  mma_commit(&bar_odone[g]);
+                else
+                  issue_s(at % C::RING, j + 2 == nt);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
         }
-        u += n;
         ok = ok && skip_to(m);
       }
       if (elect_one()) {
@@ -689,6 +711,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     }
   } else {
     // ================= softmax, rescale, epilogue: thread = row =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     const int g = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const int row_tok = row / p.G, row_head = row % p.G;
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_addr = tbase + lanes + C::S_COL + 128 * g, o_addr = tbase + lanes + C::O_COL + D * g;
     const float sc = p.scale_log2;
-    int u = 0;                 // halves done: buffer u & 1, its barriers' phase u >> 1
+    int us = 0, uo = 0;        // S tiles and O tiles read
     bool ok = true;
     for (int k = 0; ok; ++k) {
       ok = next_item(k);
@@ -709,109 +732,143 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       // keys [0, seen) of the sequence are visible to this row
       const int seen = (p.causal && !it.prefix) ? max(0, min(it.lk, it.t0 + tok + it.off + 1)) : it.lk;
       const int my_nh = it.nh[g], lo = it.lo[g], ahead = seen - lo * kPkKeys;
-      float m_use = -INFINITY, l_run = 0.f;
-      for (int h = 0; h < my_nh; ++h, ++u) {
-        const int b = u & 1;
-        const uint32_t sb = s_addr + 64 * b;
-        ok = warp_wait(&bar_sfull[g][b], (uint32_t)(u >> 1) & 1u, &abort_flag, p.limit_ns);
+      const int my_nt = (my_nh + 1) / 2;
+      float m_use = -INFINITY, l_run = 0.f, top = 0.f;   // reference, sum, maximum of the tile before
+      bool passed = false;                                 // a row's maximum has passed its reference
+      const int whole = __reduce_min_sync(0xffffffffu, ahead);   // keys that all rows of the warp see
+      for (int j = 0; j < my_nt; ++j) {
+        ok = warp_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, p.limit_ns);
         if (!ok) break;
-        tc_fence_after();
-        if (warp_live) {
-          uint32_t sv[64];
-          uint32_t (&s_lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[0]);
-          uint32_t (&s_hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[32]);
-          tmem_ld32(sb, s_lo);
-          tmem_ld32(sb + 32, s_hi);
-          tmem_wait_ld();
-          reg_fence32(s_lo);
-          reg_fence32(s_hi);
-          const int nv = ahead - h * kPkHalf;               // visible columns of this half
-          if (__any_sync(0xffffffffu, nv < kPkHalf)) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= nv) sv[c] = 0xFF800000u;             // -inf
+        const bool two = 2 * j + 1 < my_nh;
+        if (!warp_live) {          // no rows: the scores only have to be handed back
+          if (lane == 0) {
+            mbar_arrive(&bar_pfull[g][0]);
+            if (two) mbar_arrive(&bar_pfull[g][1]);
           }
-          const float* f = reinterpret_cast<const float*>(sv);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sv[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+        if (j * kPkKeys + kPkKeys > whole) {              // some row does not see all of this tile
+          const int nv = ahead - j * kPkKeys;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= nv) sv[c] = 0xFF800000u;             // -inf
+        }
+        const float* f = reinterpret_cast<const float*>(sv);
+        auto maximum = [&]() {
           float t8[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float a = fmax3(f[i], f[i + 8], f[i + 16]);
-            a = fmax3(a, f[i + 24], f[i + 32]);
-            a = fmax3(a, f[i + 40], f[i + 48]);
-            t8[i] = fmaxf(a, f[i + 56]);
-          }
-          const float mx = fmaxf(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], fmax3(t8[5], t8[6], t8[7]))) * sc;
-          const bool grow = mx > m_use + kPkLazy;           // also the first finite maximum
-          if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? ex2f(m_use - mx) : 1.f;   // 0 from -inf
-            if (grow) m_use = mx;
-            l_run *= alpha;
-            if (h > 0) {
-              // the product of the half before must be in O
-              ok = warp_wait(&bar_pvdone[g][b ^ 1], (uint32_t)((u - 1) >> 1) & 1u, &abort_flag, p.limit_ns);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t a2 = f2pack(alpha, alpha);
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_addr + c, o);
-                tmem_wait_ld();
-                reg_fence32(o);
+            float a = fmaxf(f[i], f[i + 8]);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float x, y;
-                  f2unpack(mul2(f2pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x, y);
-                  o[i] = __float_as_uint(x);
-                  o[i + 1] = __float_as_uint(y);
-                }
-                tmem_st32(o_addr + c, o);
-              }
-            }
+            for (int c = 16; c < 112; c += 16) a = fmax3(a, f[i + c], f[i + c + 8]);
+            t8[i] = fmax3(a, f[i + 112], f[i + 120]);
           }
+          return fmaxf(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], fmax3(t8[5], t8[6], t8[7]))) * sc;
+        };
+        // takes `top` as the reference of the rows that it has passed, and the sums with it
+        auto move = [&]() {
+          const bool grow = top > m_use + kPkLazy;        // also the first finite maximum
+          const float alpha = grow ? ex2f(m_use - top) : 1.f;   // 0 from -inf
+          if (grow) m_use = top;
+          l_run *= alpha;
+          if (j == 0) return;
+          const uint64_t a2 = f2pack(alpha, alpha);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float x, y;
+              f2unpack(mul2(f2pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x, y);
+              o[i] = __float_as_uint(x);
+              o[i + 1] = __float_as_uint(y);
+            }
+            tmem_st32(o_addr + c, o);
+          }
+        };
+        top = maximum();
+        if (__any_sync(0xffffffffu, top > m_use + kPkLazy)) move();
+        uint32_t pk[32];
+        uint64_t sum2[4];
+        // P of columns [from, from + 2 pairs): exponentials, their sums, bf16 pairs
+        auto exponentials = [&](int from, int pairs) {
           const float at = m_use == -INFINITY ? 0.f : m_use;  // nothing visible yet: exp2(-inf - 0) = 0
           const uint64_t sc2 = f2pack(sc, sc), nm2 = f2pack(-at, -at);
-          uint64_t sum2[4] = {0, 0, 0, 0};
-          uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
+          for (int i = 0; i < pairs; ++i) {
+            const int c = from + 2 * i;
             float x0, x1;
-            f2unpack(fma2(f2pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, nm2), x0, x1);
+            f2unpack(fma2(f2pack(f[c], f[c + 1]), sc2, nm2), x0, x1);
             const float p0 = ex2f(x0), p1 = ex2f(x1);
-            sum2[(c >> 1) & 3] = add2(sum2[(c >> 1) & 3], f2pack(p0, p1));
+            sum2[i & 3] = add2(sum2[i & 3], f2pack(p0, p1));
             const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
-            pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
+            pk[(c & 63) >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
           }
-          tmem_st32(sb, pk);
-          float a0, a1, b0, b1;
-          f2unpack(add2(sum2[0], sum2[1]), a0, a1);
-          f2unpack(add2(sum2[2], sum2[3]), b0, b1);
-          l_run += (a0 + a1) + (b0 + b1);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum2[i] = 0;
+        exponentials(0, 32);
+        tmem_st32(s_addr, pk);
+        if (two) {
+          // the first half is on its way while the second starts
+          exponentials(64, 8);
           tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_pfull[g][0]);
+          exponentials(80, 24);
+          tmem_st32(s_addr + 64, pk);
         }
+        float a0, a1, b0, b1;
+        f2unpack(add2(sum2[0], sum2[1]), a0, a1);
+        f2unpack(add2(sum2[2], sum2[3]), b0, b1);
+        l_run += (a0 + a1) + (b0 + b1);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_pfull[g][b]);
+        if (lane == 0) mbar_arrive(&bar_pfull[g][two ? 1 : 0]);
       }
       if (ok && my_nh > 0) {
-        ok = warp_wait(&bar_pvdone[g][(u - 1) & 1], (uint32_t)((u - 1) >> 1) & 1u, &abort_flag, p.limit_ns);
+        ok = warp_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, p.limit_ns);
         tc_fence_after();
       }
-      if (!ok) break;
-      if (!warp_live) {
+      if (ok && !warp_live) {
         done_item(k);
         continue;
       }
+      if (!ok) break;
       const int head = it.head * p.G + row_head;
       const int from = lo * kPkKeys;                          // keys [from, to) were computed
       const int to = min(it.lk, from + my_nh * kPkHalf);
       const bool any = valid && seen > from && my_nh > 0;        // this row saw a key
       const float inv = slot < 0 ? 1.0f / l_run : 1.0f;
       const long long tr = it.q0 + tok;
-      __nv_bfloat16* orow = p.o + head * p.osH + tr * p.osL;
       const long long R = (long long)p.Tq * p.Hkv * p.G, prow = slot * R + tr * (p.Hkv * p.G) + head;
-      float* part = slot < 0 ? nullptr : p.part + prow * D;
       float check = 0.f;
+      // where all rows of a warp are live, four lanes write 64 neighbouring bytes of a row, not
+      // one lane 16 of its own (half a sector): cross-attention 175 -> 152 us; few rows are
+      // written as they lie, which takes fewer instructions
+      const bool full = __all_sync(0xffffffffu, valid);
+      __nv_bfloat16* to_row[4];
+      float* to_part[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int src = (lane & 28) + w, piece = full ? lane & 3 : w;
+        const int h2 = full ? __shfl_sync(0xffffffffu, head, src) : head;
+        const long long t2 = full ? it.q0 + __shfl_sync(0xffffffffu, tok, src) : tr;
+        to_row[w] = p.o + h2 * p.osH + t2 * p.osL + 8 * piece;
+        to_part[w] = p.part + (slot * R + t2 * (p.Hkv * p.G) + h2) * D + 4 * piece;
+      }
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -826,23 +883,35 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           check = fmaf(x, 0.f, check);
           o[i] = __float_as_uint(any ? x * inv : 0.f);
         }
-        if (!valid) continue;
         if (slot < 0) {
+          uint4 h[4];            // this row's 32 channels
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint32_t h[4];
+            uint32_t y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const __nv_bfloat162 hb = __floats2bfloat162_rn(__uint_as_float(o[8 * w + 2 * i]),
                                                               __uint_as_float(o[8 * w + 2 * i + 1]));
-              h[i] = *reinterpret_cast<const uint32_t*>(&hb);
+              y[i] = *reinterpret_cast<const uint32_t*>(&hb);
             }
-            *reinterpret_cast<uint4*>(orow + c + 8 * w) = make_uint4(h[0], h[1], h[2], h[3]);
+            h[w] = make_uint4(y[0], y[1], y[2], y[3]);
           }
+          if (full) transpose4(h);   // h[w]: piece lane % 4 of row (lane & 28) + w
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (valid) *reinterpret_cast<uint4*>(to_row[w] + c) = h[w];
         } else {
 #pragma unroll
-          for (int w = 0; w < 8; ++w)
-            *reinterpret_cast<uint4*>(part + c + 4 * w) = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+          for (int y = 0; y < 2; ++y) {
+            uint4 h[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              h[w] = make_uint4(o[16 * y + 4 * w], o[16 * y + 4 * w + 1], o[16 * y + 4 * w + 2], o[16 * y + 4 * w + 3]);
+            if (full) transpose4(h);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (valid) *reinterpret_cast<uint4*>(to_part[w] + c + 16 * y) = h[w];
+          }
         }
       }
       if (valid) {

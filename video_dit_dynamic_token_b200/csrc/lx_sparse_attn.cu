@@ -384,8 +384,8 @@ struct PackWs {
 };
 PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D, int64_t Tk, bool prefix) {
   PackWs w{};
-  // no sequence is longer than the shortest split: nothing to join
-  if (!prefix && Tk <= lx::kPkSplitKeys * lx::kPkKeys) {
+  // no sequence is longer than two tiles: joining would cost more than it saves
+  if (!prefix && Tk <= 2 * lx::kPkKeys) {
     w.splits = 1;
     return w;
   }
@@ -413,8 +413,8 @@ lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t
   using C = lx::PackCfg<D>;
   // upper bounds: the lengths are on the device.  Splits add less than a round for every
   // SM three times over (items of at least a third of a CTA's share of the work).
-  const int64_t rows = 2 * p.TQ, tiles = p.Tq / rows + std::min(p.n, p.Tq);
-  const int64_t prefix = p.Lp ? p.Tq / rows + 1 : 0, splits = p.part ? 3 * (lx::kPkSMs + p.Hkv) : 0;
+  const int64_t rows = 2 * p.TQ, tiles = p.Tq / rows + std::min(p.n, p.Tq), prefix = p.Lp ? p.Tq / rows + 1 : 0;
+  const int64_t splits = p.part ? 3 * (lx::kPkSMs + p.units) : 0;
   const int64_t items = splits + (tiles + prefix) * p.Hkv, blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
   if (items > 0x7FFFFFFE || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(lx::packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
@@ -452,8 +452,11 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
       p.ml = reinterpret_cast<float2*>(base + w.ml);
       p.part = reinterpret_cast<float*>(base + w.part);
     }
-    p.max_np = Kp ? (int)(w.splits / 2) : 0;
-    p.max_ns = (int)(w.splits - p.max_np);
+    // shared out between the prefix and the sequences, but no more than keys to split
+    auto most = [](int64_t keys) { return std::max<int64_t>(1, (keys + lx::kPkKeys - 1) / lx::kPkKeys); };
+    const int64_t np = Kp ? std::min(w.splits / 2, most(Kp->L)) : 0;
+    p.max_ns = (int)std::min(w.splits - np, most(K->L));
+    p.max_np = Kp ? (int)(w.splits - p.max_ns) : 0;
   }
   p.cu_q = pack->cu_q;
   p.cu_k = pack->cu_k;
@@ -467,10 +470,12 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   p.TQ = pack_tokens(G);
   p.causal = causal != 0;
   p.scale_log2 = (float)(1.4426950408889634 * (double)scale);
-  // heads at a time: as many as keep K and V within half of the 126 MB L2, in even groups
-  const int64_t fit = std::max<int64_t>(1, ((int64_t)63 << 20) / (4 * (K->L + p.Lp) * Q->D));
-  const int64_t groups = (K->H + fit - 1) / fit;
-  p.group = (int)((K->H + groups - 1) / groups);
+  p.pair = K->H % 2 == 0 ? 2 : 1;
+  p.units = (int)(K->H / p.pair);
+  // units at a time: as many as keep K and V within half of the 126 MB L2, in even groups
+  const int64_t fit = std::max<int64_t>(1, ((int64_t)63 << 20) / (4 * p.pair * (K->L + p.Lp) * Q->D));
+  const int64_t groups = (p.units + fit - 1) / fit;
+  p.group = (int)((p.units + groups - 1) / groups);
   p.q = view(Q);
   p.k = view(K);
   p.v = view(V);

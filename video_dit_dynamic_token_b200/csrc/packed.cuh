@@ -14,9 +14,12 @@
 //
 // A work item keeps two streams of a CTA busy, each with a row tile of Q, its
 // softmax warpgroup and its accumulator in TMEM; while one stream's softmax runs, the
-// tensor core works for the other.  A sequence of more than TQ tokens gives each stream a
-// row tile of its own and both the same 128-key tiles (loaded once); a shorter one, such
-// as a single token, gives both the same rows and each a range of keys of its own.
+// tensor core works for the other.  Two row tiles of a sequence (2 TQ tokens) share
+// the same 128-key tiles, loaded once.  A single row tile (narrow), such as a single token or
+// the rest of a longer sequence, is taken for two neighbouring key/value heads; where their
+// number is odd, for one, whose keys are split between the streams.  (Splitting for all:
+// decoding 48 sequences 113 us instead of 108, 64 behind a prefix 58 instead of 52; pairs
+// for an odd number, the last one half empty: 39 instead of 31 us with one head.)
 // Key ranges (splits) also spread long sequences over the SMs when there are few items:
 // a split leaves its unnormalised fp32 rows and (max, sum), and packed_combine_kernel
 // joins them.  A row whose keys are one split is finished by its item.
@@ -40,12 +43,10 @@
 // for its own hand-over.)
 //
 // The reference that the exponents are taken against is not the running maximum but
-// follows it: it moves when the maximum has passed it by more than 2^8, and the maximum
-// of a tile counts from the next tile on, so that the exponentials do not wait for it (a
-// shift leaves the quotient unchanged: P's rounding to bf16 is relative, and a tile
-// whose scores pass the reference by 2^16 gets a new one at once).  O is
-// rarely rescaled.  P is rounded to bf16, the type of V and of the output; the row sum
-// takes the unrounded fp32 values.
+// follows it: it moves only when the maximum of a tile has passed it by more than 2^8, so
+// that O is rarely rescaled.  A shift leaves the quotient unchanged: P is at most 2^8 and its
+// rounding to bf16, the type of V and of the output, is relative; the row sum takes the
+// unrounded fp32 values.
 //
 // Values in masked places: scores are replaced by -inf by selection, and V rows
 // past a sequence's end are zeroed in shared memory before they are used.  A
@@ -64,12 +65,11 @@ namespace lx {
 
 constexpr int kPkKeys = 128;         // keys of a tile
 constexpr int kPkHalf = 64;          // keys of a product with V
-constexpr int kPkSplitKeys = 2;      // a split covers at least this many tiles
+constexpr int kPkSplitKeys = 1;      // a split covers at least this many tiles (2: four tokens behind 200 keys 15.9, not 14.1 us)
 constexpr int kPkFine = 6;           // from this many tiles on, three splits for a CTA's share of the work
 constexpr int kPkSMs = 148;
 constexpr int kPkItems = 4;          // items published ahead of their last reader
 constexpr float kPkLazy = 8.0f;      // log2 growth of the row maximum that moves the reference
-constexpr float kPkFar = 16.0f;      // log2 distance from the reference that a tile may have
 
 template <int D>
 struct PackCfg {
@@ -105,7 +105,8 @@ struct PackParams {
   float2* ml;            // [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
   int* chunk;            // tiles per split, for the combine kernel
   int max_np, max_ns;    // most splits of the prefix, of a sequence
-  int group;             // key/value heads worked on at a time
+  int pair, units;       // key/value heads of a narrow item (1 or 2), Hkv / pair
+  int group;             // units worked on at a time
   unsigned long long limit_ns;
 };
 
@@ -143,15 +144,20 @@ __device__ __forceinline__ PackSeq pack_all(const PackParams& p) {
 
 __device__ __forceinline__ int pack_div(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int pack_tiles(int keys) { return (keys + kPkKeys - 1) / kPkKeys; }
-// Splits of T key tiles, c tiles each and at most `most`.  Rows that fit one row tile
-// (narrow) have two streams to feed: at least two splits, where these are long enough.
-__device__ __forceinline__ int pack_splits(int T, bool narrow, int c, int most) {
-  if (narrow) c = min(c, max(kPkSplitKeys, pack_div(T, 2)));
+// Row tile pairs of `rows` tokens; a rest of at most TQ tokens is a narrow item.
+__device__ __forceinline__ int pack_pairs(const PackParams& p, int rows) { return (rows + p.TQ - 1) / (2 * p.TQ); }
+__device__ __forceinline__ int pack_narrow(const PackParams& p, int rows) {
+  return rows > 2 * p.TQ * pack_pairs(p, rows) ? 1 : 0;
+}
+// Splits of T key tiles, c tiles each and at most `most`; at least two where the streams
+// of a narrow item share a head and all rows are in it.
+__device__ __forceinline__ int pack_splits(const PackParams& p, int rows, int T, int c, int most) {
+  if (p.pair == 1 && rows <= p.TQ) c = min(c, max(kPkSplitKeys, pack_div(T, 2)));
   return max(1, min(most, pack_div(T, c)));
 }
-// Items of `rows` tokens over T key tiles in ns splits.
-__device__ __forceinline__ int pack_count(int rows, int TQ, int ns) {
-  return rows <= TQ ? (rows > 0 ? pack_div(ns, 2) : 0) : pack_div(rows, 2 * TQ) * ns;
+// Items of `rows` tokens in ns splits, for p.pair heads together.
+__device__ __forceinline__ int pack_count(const PackParams& p, int rows, int ns) {
+  return p.pair * pack_pairs(p, rows) * ns + pack_narrow(p, rows) * (p.pair == 2 ? ns : pack_div(ns, 2));
 }
 
 struct PackItem {
@@ -161,35 +167,35 @@ struct PackItem {
   int lo[2], nt[2];      // first key tile and number of key tiles of each stream
   int nh[2];             // number of halves with a key that some row sees
   int slot[2];           // where a stream's partial result goes; -1: it finishes its rows; -2: no rows
-  int head;              // key/value head
+  int head[2];           // key/value head of each stream
   int prefix;            // keys of the prefix (no causal rule)
-  int narrow;            // both streams have the item's rows and keys of their own
+  int narrow;            // both streams have the item's rows, and a head or a range of keys each
   int stop;              // no further item
 };
 
-// What a CTA works out once from the sequence table: the number of items per
-// key/value head, and for up to 128 chunks of sequences the items before each.
+// What a CTA works out once from the sequence table: the number of items of a unit
+// (p.pair key/value heads), and for up to 128 chunks of sequences the items before each.
 constexpr int kPkChunks = 128;
 struct PackTable {
   unsigned long long work;
   int longest;
   int c, np, pi;           // tiles per split, prefix splits, prefix items
-  int total;               // items of a head
+  int total;               // items of a unit
   int before[kPkChunks + 1];
 };
 
 // Splits and items of a sequence.
 __device__ __forceinline__ int pack_seq_splits(const PackParams& p, const PackSeq& s, int c) {
-  return pack_splits(pack_tiles(s.lk), s.lq <= p.TQ, c, p.max_ns);
+  return pack_splits(p, s.lq, pack_tiles(s.lk), c, p.max_ns);
 }
 __device__ __forceinline__ int pack_seq_items(const PackParams& p, const PackSeq& s, int c) {
   if (p.Lp && s.lk == 0) return 0;   // behind a prefix a sequence may have no keys of its own
-  return pack_count(s.lq, p.TQ, pack_seq_splits(p, s, c));
+  return pack_count(p, s.lq, pack_seq_splits(p, s, c));
 }
-// Steps of a CTA over T key tiles for `rows` tokens.
+// Steps of a CTA over T key tiles for `rows` tokens of p.pair heads.
 __device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, int rows, int T) {
-  if (rows <= 0) return 0;
-  return rows <= p.TQ ? (T + 1) / 2 : (unsigned long long)pack_div(rows, 2 * p.TQ) * T;
+  return (unsigned long long)(p.pair * pack_pairs(p, rows)) * T +
+         pack_narrow(p, rows) * (p.pair == 2 ? T : (T + 1) / 2);
 }
 
 // Every thread reads a share of the table, so that lengths stay on the device.
@@ -221,15 +227,15 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
     __syncthreads();
     if (tid == 0) {
       const int pt = pack_tiles(p.Lp), rows = p.Lp ? pack_all(p).lq : 0;
-      const unsigned long long work = (tb.work + pack_steps(p, rows, pt)) * p.Hkv;
+      const unsigned long long work = (tb.work + pack_steps(p, rows, pt)) * p.units;
       int c = (int)((work + kPkSMs - 1) / kPkSMs);
       if (c > kPkFine) c = max(kPkFine, pack_div(c, 3));
       c = max(max(c, kPkSplitKeys), pack_div(tb.longest, p.max_ns));
       if (p.Lp) c = max(c, pack_div(pt, p.max_np));
       tb.c = c;
       if (p.Lp) {
-        tb.np = pack_splits(pt, rows <= p.TQ, c, p.max_np);
-        tb.pi = pack_count(rows, p.TQ, tb.np);
+        tb.np = pack_splits(p, rows, pt, c, p.max_np);
+        tb.pi = pack_count(p, rows, tb.np);
       }
       if (blockIdx.x == 0) *p.chunk = c;
     }
@@ -258,19 +264,19 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   __syncthreads();
 }
 
-// Item number `id` (a warp together); stop past the last one.  In the order of a head's
+// Item number `id` (a warp together); stop past the last one.  In the order of a unit's
 // items the prefix comes first, then the last rows of the last sequence (with the causal
-// rule the long items start first); p.group heads, whose K and V fit the L2 cache
+// rule the long items start first); p.group units, whose K and V fit the L2 cache
 // together, take turns in it.
 __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& tb, int id, PackItem& it) {
   const int lane = threadIdx.x & 31;
   it.stop = 1;
-  if (id / p.Hkv >= tb.total) return;   // total * Hkv items in all
+  if (id / p.units >= tb.total) return;   // total * units items in all
   it.stop = 0;
-  const int first_head = id / (tb.total * p.group) * p.group, heads = min(p.group, p.Hkv - first_head);
-  id -= first_head * tb.total;
-  it.head = first_head + id % heads;
-  int x = id / heads;
+  const int first = id / (tb.total * p.group) * p.group, turns = min(p.group, p.units - first);
+  id -= first * tb.total;
+  const int unit = first + id % turns;
+  int x = id / turns;
   PackSeq s{0, 0, 0, 0};
   int ns, base = -1;                    // splits; slot of the first one
   it.prefix = x < tb.pi;
@@ -311,10 +317,13 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
     ns = pack_seq_splits(p, s, tb.c);
     if (p.Lp || ns > 1) base = tb.np;
   }
-  const int T = pack_tiles(s.lk), per = pack_div(T, ns);
-  it.narrow = s.lq <= p.TQ;
-  const int tile = it.narrow ? 0 : x / ns;
-  it.t0 = tile * 2 * p.TQ;
+  const int T = pack_tiles(s.lk), per = pack_div(T, ns), pairs = pack_pairs(p, s.lq);
+  // first the pairs of row tiles, then the narrow rest; sequences are walked from the end,
+  // so that the order within one is turned round as well
+  const int wide = p.pair * pairs * ns, two = p.pair - 1;
+  it.narrow = x >= wide;
+  const int y = it.narrow ? x - wide : x >> two;
+  it.t0 = (it.narrow ? pairs : y / ns) * 2 * p.TQ;
   it.q0 = s.q0 + it.t0;
   it.q_end = s.q0 + s.lq;
   it.off = s.lk - s.lq;
@@ -322,12 +331,14 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
   it.lk = s.lk;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int sp = it.narrow ? 2 * x + g : x % ns, first = it.narrow ? 0 : g * p.TQ;
-    const int tokens = min(p.TQ, it.q_end - it.q0 - first);
-    int lo = min(sp * per, T), hi = min(lo + per, T);
+    const int first_tok = it.narrow ? 0 : g * p.TQ;
+    const int tokens = min(p.TQ, it.q_end - it.q0 - first_tok);
+    const int sp = !it.narrow ? y % ns : (two ? y : 2 * y + g);
+    it.head[g] = p.pair * unit + (two & (it.narrow ? g : x));
+    const int lo = min(sp * per, T), hi = min(lo + per, T);
     // keys up to the last one that the tile's last token sees
     int keys = min(s.lk, hi * kPkKeys);
-    if (p.causal && !it.prefix) keys = min(keys, it.t0 + first + tokens + it.off);
+    if (p.causal && !it.prefix) keys = min(keys, it.t0 + first_tok + tokens + it.off);
     const bool live = tokens > 0 && sp < ns;
     it.lo[g] = lo;
     it.nh[g] = live ? pack_div(max(0, keys - lo * kPkKeys), kPkHalf) : 0;
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int TMA_WARP = 4 * NQ, MMA_WARP = 4 * NQ + 1;
   pack_prepare<C::THREADS>(p, table);
-  if ((int)blockIdx.x / p.Hkv >= table.total) return;   // the grid is an upper bound
+  if ((int)blockIdx.x / p.units >= table.total) return;   // the grid is an upper bound
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::RING; ++s) {
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
             mbar_arrive_expect_tx(&bar_qfull[g], (uint32_t)(C::NATOM * p.G * p.TQ * 128));
             for (int a = 0; a < C::NATOM; ++a)
               tma_load_4d(sm + g * C::TILE_BYTES + a * 128 * 128, &tmQ, &bar_qfull[g], a * 64, 0,
-                          it.q0 + (it.narrow ? 0 : g * p.TQ), it.head);
+                          it.q0 + (it.narrow ? 0 : g * p.TQ), it.head[g]);
           }
           __syncwarp();
           ++uq[g];
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         if (!ok) break;
         // shared key tiles: K(j), V(j); of its own for each stream: K_0(j), K_1(j), V_0(j), V_1(j)
         const int most = max(it.nt[0], it.nt[1]);
-        auto load = [&](const CUtensorMap* map, int tile) {
+        auto load = [&](const CUtensorMap* map, int j, int g) {
           const int slot = m % C::RING;
           if (m >= C::RING &&
               !warp_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, p.limit_ns))
@@ -554,7 +565,8 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
             uint8_t* dst = sm + C::OFF_RING + slot * C::TILE_BYTES;
             mbar_arrive_expect_tx(&bar_full[slot], C::TILE_BYTES);
             for (int a = 0; a < C::NATOM; ++a)
-              tma_load_4d(dst + a * 128 * 128, map, &bar_full[slot], a * 64, it.k0 + tile * kPkKeys, it.head, 0);
+              tma_load_4d(dst + a * 128 * 128, map, &bar_full[slot], a * 64, it.k0 + (it.lo[g] + j) * kPkKeys,
+                          it.head[g], 0);
           }
           __syncwarp();
           ++m;
@@ -562,11 +574,10 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         };
         for (int j = 0; ok && j < most; ++j) {
           if (!it.narrow) {
-            ok = load(mk, it.lo[0] + j) && load(mv, it.lo[0] + j);
+            ok = load(mk, j, 0) && load(mv, j, 0);
           } else {
             const bool b1 = j < it.nt[1];
-            ok = load(mk, it.lo[0] + j) && (!b1 || load(mk, it.lo[1] + j)) && load(mv, it.lo[0] + j) &&
-                 (!b1 || load(mv, it.lo[1] + j));
+            ok = load(mk, j, 0) && (!b1 || load(mk, j, 1)) && load(mv, j, 0) && (!b1 || load(mv, j, 1));
           }
         }
         if (!ok) break;
@@ -733,8 +744,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       const int seen = (p.causal && !it.prefix) ? max(0, min(it.lk, it.t0 + tok + it.off + 1)) : it.lk;
       const int my_nh = it.nh[g], lo = it.lo[g], ahead = seen - lo * kPkKeys;
       const int my_nt = (my_nh + 1) / 2;
-      float m_use = -INFINITY, l_run = 0.f, top = 0.f;   // reference, sum, maximum of the tile before
-      bool passed = false;                                 // a row's maximum has passed its reference
+      float m_use = -INFINITY, l_run = 0.f, top;   // reference, sum, maximum of the tile
       const int whole = __reduce_min_sync(0xffffffffu, ahead);   // keys that all rows of the warp see
       for (int j = 0; j < my_nt; ++j) {
         ok = warp_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, p.limit_ns);
@@ -847,7 +857,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         continue;
       }
       if (!ok) break;
-      const int head = it.head * p.G + row_head;
+      const int head = it.head[g] * p.G + row_head;
       const int from = lo * kPkKeys;                          // keys [from, to) were computed
       const int to = min(it.lk, from + my_nh * kPkHalf);
       const bool any = valid && seen > from && my_nh > 0;        // this row saw a key
@@ -927,8 +937,8 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         redo &= redo - 1;
         const int s_seen = __shfl_sync(0xffffffffu, seen, src), s_head = __shfl_sync(0xffffffffu, head, src);
         const int s_tr = __shfl_sync(0xffffffffu, (int)tr, src);
-        const __nv_bfloat16* kb = p.k.p + it.head * p.k.sH + (long long)it.k0 * p.k.sL;
-        const __nv_bfloat16* vb = p.v.p + it.head * p.v.sH + (long long)it.k0 * p.v.sL;
+        const __nv_bfloat16* kb = p.k.p + it.head[g] * p.k.sH + (long long)it.k0 * p.k.sL;
+        const __nv_bfloat16* vb = p.v.p + it.head[g] * p.v.sH + (long long)it.k0 * p.v.sL;
         constexpr int E = D / 32;
         bool spoilt = false;
         for (int u = s_seen; u < to; ++u)
@@ -999,7 +1009,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
     rows = all.lq;
   }
   const int c = *p.chunk;
-  const int np = p.Lp ? pack_splits(pack_tiles(p.Lp), rows <= p.TQ, c, p.max_np) : 0;
+  const int np = p.Lp ? pack_splits(p, rows, pack_tiles(p.Lp), c, p.max_np) : 0;
   const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
   if (!p.Lp && ns == 1) return;   // its item finished the row
   float m = -INFINITY;

@@ -420,11 +420,24 @@ lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t
   if (cudaFuncSetAttribute(lx::packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
     return LX_ERR_CUDA;
-  lx::packed_attn_kernel<D><<<(unsigned)items, C::THREADS, C::SMEM, s>>>(t[0], t[1], t[2], t[3], t[4], p);
-  lx_status st = launch_status();
-  if (st != LX_OK || !p.part) return st;
-  lx::packed_combine_kernel<D><<<(unsigned)blocks, 256, 0, s>>>(p);
-  return launch_status();
+  // both kernels start while the work ahead of them ends (they wait for it themselves)
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, lx::packed_attn_kernel<D>, t[0], t[1], t[2], t[3], t[4], p) != cudaSuccess)
+    return LX_ERR_CUDA;
+  if (!p.part) return launch_status();
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, lx::packed_combine_kernel<D>, p) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
 }
 
 // Both entry points: Kp, Vp null without a prefix.

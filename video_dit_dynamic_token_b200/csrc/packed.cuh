@@ -458,9 +458,6 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int TMA_WARP = 4 * NQ, MMA_WARP = 4 * NQ + 1;
-  pack_prepare<C::THREADS>(p, table);
-  if ((int)blockIdx.x / p.units >= table.total) return;   // the grid is an upper bound
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::RING; ++s) {
       mbar_init(&bar_full[s], 1);
@@ -483,6 +480,10 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     never_abort = 0;
     fence_barrier_init();
   }
+  // the work ahead of this kernel may still run up to here
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pack_prepare<C::THREADS>(p, table);
+  if ((int)blockIdx.x / p.units >= table.total) return;   // the grid is an upper bound
   if (warp == MMA_WARP) {
     tmem_alloc(&tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
@@ -589,6 +590,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         id = next < 0 ? 0x7FFFFFFF : next;
         __syncwarp();
       }
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // no block is left to start
       if (leader) {
         if (!ok) {
           abort_flag = 1;
@@ -988,6 +990,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
   constexpr int E = D / 32;
   const int Hq = p.Hkv * p.G, lane = threadIdx.x & 31;
   const long long R = (long long)p.Tq * Hq, row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");   // the partial rows are complete
   if (row >= R) return;
   const int tok = (int)(row / Hq), head = (int)(row % Hq);
   // the last sequence that starts at or before this token

@@ -555,6 +555,8 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
     N = wq.R
     if K != wq.K:
         raise ValueError("x and W differ in K")
+    if wq.codes.numel() * 2 != N * K or wq.sf.numel() < (N + 127) // 128 * 8 * K:
+        raise ValueError("W: not the codes and scales of an [N, K] tensor")
     if out is None:
         out = x.new_empty((M, N))
     elif out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:

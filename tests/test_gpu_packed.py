@@ -333,3 +333,29 @@ def test_rows_far_into_a_long_cache(lx):
     assert lx.lx_last_device_status() == 0
     _check(o, lse, oracle.packed_attn_ref(_np(Q), _np(K[:, :, a:a + n]), _np(V[:, :, a:a + n]), [0, 3], [0, n], True,
                                           D ** -0.5), D)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,prefix", [(6, 6, 0), (5, 5, 0), (10, 2, 0), (9, 3, 0), (12, 4, 700), (15, 3, 700), (4, 1, 700)])
+def test_rests_of_one_row_tile(lx, hq, hkv, prefix, causal):
+    """Sequences that end in a single row tile, with even and odd numbers of key/value heads, split and whole."""
+    tq = 128 // (hq // hkv)
+    lens = [2 * tq + 1, 3 * tq, 2 * tq + tq // 2, tq, tq + 1, 4 * tq]
+    _run(lx, lens, [n + 300 for n in lens], hq, hkv, 64, causal, seed=hq + prefix, prefix=prefix, spare=3)
+
+
+@pytest.mark.parametrize("pad", [8, 16])
+def test_rows_of_the_output_at_16_and_32_bytes(lx, pad):
+    gen = torch.Generator().manual_seed(38)
+    lq = [130, 1, 40]
+    Q, K, V = (_rows(gen, 4, 171, 64, token_major=False) for _ in range(3))
+    cu = _cu(lq)
+    room = torch.full((1, 4, 171, 64 + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+    for first in (0, pad):
+        out, lse = room[..., first:first + 64], torch.empty((4, 171), device=DEV)
+        lx.lx_attn_packed(Q, K, V, _i32(cu), _i32(cu), out=out, lse=lse)
+        assert lx.lx_last_device_status() == 0
+        _check(out, lse, oracle.packed_attn_ref(_np(Q), _np(K), _np(V), cu, cu, True, 64 ** -0.5), 64)
+        rest = torch.cat((room[..., :first], room[..., first + 64:]), -1)
+        assert torch.all(rest == 7.0)
+        room.fill_(7.0)

@@ -495,6 +495,7 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   p.o = reinterpret_cast<__nv_bfloat16*>(O->data);
   p.osH = O->sH;
   p.osL = O->sL;
+  p.sectors = ((reinterpret_cast<uintptr_t>(O->data) | (uintptr_t)(2 * O->sH) | (uintptr_t)(2 * O->sL)) & 31u) == 0;
   p.lse = lse;
   p.limit_ns = kWaitLimitNs;
   CUtensorMap t[5];

@@ -100,6 +100,7 @@ struct PackParams {
   BhldView q, k, v;      // for packed_exact_row
   __nv_bfloat16* o;
   long long osH, osL;
+  int sectors;           // rows of o start at multiples of 32 bytes
   float* lse;            // [Hq][Tq] or null
   float* part;           // [max_np + max_ns][Tq * Hq][D] unnormalised rows; null where nothing is split
   float2* ml;            // [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
@@ -400,6 +401,13 @@ __device__ __forceinline__ void transpose4(uint4 (&h)[4]) {
   swap(h[2], h[3], 1, lane & 1);
   swap(h[0], h[2], 2, lane & 2);
   swap(h[1], h[3], 2, lane & 2);
+}
+
+// 32 bytes, a whole sector (the address a multiple of 32).
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 
 // One row over keys [lo, hi), a warp together: lane holds D / 32 neighbouring
@@ -863,24 +871,15 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       const int from = lo * kPkKeys;                          // keys [from, to) were computed
       const int to = min(it.lk, from + my_nh * kPkHalf);
       const bool any = valid && seen > from && my_nh > 0;        // this row saw a key
-      const float inv = slot < 0 ? 1.0f / l_run : 1.0f;
       const long long tr = it.q0 + tok;
       const long long R = (long long)p.Tq * p.Hkv * p.G, prow = slot * R + tr * (p.Hkv * p.G) + head;
+      // rows without a key, rows with hidden keys: neither in most items
+      const bool odd = !__all_sync(0xffffffffu, any || !valid) || __any_sync(0xffffffffu, any && seen < to);
       float check = 0.f;
-      // where all rows of a warp are live, four lanes write 64 neighbouring bytes of a row, not
-      // one lane 16 of its own (half a sector): cross-attention 175 -> 152 us; few rows are
-      // written as they lie, which takes fewer instructions
-      const bool full = __all_sync(0xffffffffu, valid);
-      __nv_bfloat16* to_row[4];
-      float* to_part[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int src = (lane & 28) + w, piece = full ? lane & 3 : w;
-        const int h2 = full ? __shfl_sync(0xffffffffu, head, src) : head;
-        const long long t2 = full ? it.q0 + __shfl_sync(0xffffffffu, tok, src) : tr;
-        to_row[w] = p.o + h2 * p.osH + t2 * p.osL + 8 * piece;
-        to_part[w] = p.part + (slot * R + t2 * (p.Hkv * p.G) + h2) * D + 4 * piece;
-      }
+      const float inv = any ? 1.0f / l_run : 0.f;
+      const uint64_t inv2 = f2pack(inv, inv);
+      __nv_bfloat16* to_row = p.o + head * p.osH + tr * p.osL;
+      float* to_part = p.part + prow * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -889,41 +888,39 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           tmem_wait_ld();
           reg_fence32(o);
         }
+        if (odd) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float x = any ? __uint_as_float(o[i]) : 0.f;
-          check = fmaf(x, 0.f, check);
-          o[i] = __float_as_uint(any ? x * inv : 0.f);
+          for (int i = 0; i < 32; ++i) {
+            const float x = any ? __uint_as_float(o[i]) : 0.f;
+            check = fmaf(x, 0.f, check);
+            o[i] = __float_as_uint(x);
+          }
         }
+        // a lane writes whole 32-byte sectors of its row
         if (slot < 0) {
-          uint4 h[4];            // this row's 32 channels
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t y[4];
+          for (int w = 0; w < 2; ++w) {
+            uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 hb = __floats2bfloat162_rn(__uint_as_float(o[8 * w + 2 * i]),
-                                                              __uint_as_float(o[8 * w + 2 * i + 1]));
+            for (int i = 0; i < 8; ++i) {
+              float x0, x1;
+              f2unpack(mul2(f2pack(__uint_as_float(o[16 * w + 2 * i]), __uint_as_float(o[16 * w + 2 * i + 1])), inv2), x0, x1);
+              const __nv_bfloat162 hb = __floats2bfloat162_rn(x0, x1);
               y[i] = *reinterpret_cast<const uint32_t*>(&hb);
             }
-            h[w] = make_uint4(y[0], y[1], y[2], y[3]);
+            __nv_bfloat16* dst = to_row + c + 16 * w;
+            if (valid) {
+              if (p.sectors) {
+                st_global_32b(dst, y);
+              } else {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(dst + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
+            }
           }
-          if (full) transpose4(h);   // h[w]: piece lane % 4 of row (lane & 28) + w
+        } else if (valid) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            if (valid) *reinterpret_cast<uint4*>(to_row[w] + c) = h[w];
-        } else {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint4 h[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              h[w] = make_uint4(o[16 * y + 4 * w], o[16 * y + 4 * w + 1], o[16 * y + 4 * w + 2], o[16 * y + 4 * w + 3]);
-            if (full) transpose4(h);
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              if (valid) *reinterpret_cast<uint4*>(to_part[w] + c + 16 * y) = h[w];
-          }
+          for (int w = 0; w < 4; ++w) st_global_32b(to_part + c + 8 * w, o + 8 * w);
         }
       }
       if (valid) {

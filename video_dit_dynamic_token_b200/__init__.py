@@ -387,6 +387,7 @@ def lx_sparse_attn(Q, K, V, keep, mode="int8fp8", plan: Plan | None = None, out=
 # These calls serve single tokens, where marshalling counts: sizes of workspaces are
 # kept per shape, and the stream is asked for by device.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _with_stream(stream, t, call):
@@ -444,12 +445,12 @@ def _attn_packed(prefix, Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws
     if out is None:
         out = torch.empty_like(Q)
     dev = _same_device(Q, K, V, out, cu_q, cu_k, len_k, lse, ws, *prefix)
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _attn_packed(prefix, Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws, None)
     n = cu_q.numel() - 1
-    for t, m in ((cu_q, n + 1), (cu_k, n + 1), (len_k, n)):
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != m or not t.is_contiguous()):
+    for t, shape in ((cu_q, (n + 1,)), (cu_k, (n + 1,)), (len_k, (n,))):
+        if t is not None and (t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous()):
             raise ValueError("cu_q and cu_k: contiguous int32 tensors of n + 1 entries, len_k of n")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != Q.shape[1:3] or not lse.is_contiguous()):
         raise ValueError("lse: a contiguous fp32 [Hq, Tq] tensor")
@@ -564,7 +565,7 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != N):
         raise ValueError("bias must be a contiguous fp32 tensor of N elements")
     dev = _same_device(x, out, wq.codes, wq.sf, wq.gscale, bias, ws)
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return lx_nvfp4_gemv(x, wq, bias, out, ws)
     if ws is None:

@@ -411,11 +411,16 @@ lx_status check_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, con
 template <int D>
 lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t s) {
   using C = lx::PackCfg<D>;
-  // upper bounds: the lengths are on the device.  Splits add less than a round for every
-  // SM three times over (items of at least a third of a CTA's share of the work).
-  const int64_t rows = 2 * p.TQ, tiles = p.Tq / rows + std::min(p.n, p.Tq), prefix = p.Lp ? p.Tq / rows + 1 : 0;
-  const int64_t splits = p.part ? 3 * (lx::kPkSMs + p.units) : 0;
-  const int64_t items = splits + (tiles + prefix) * p.Hkv, blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
+  // Upper bounds: the lengths are on the device, and a block without an item costs 20 ns (512
+  // caches of 64 keys: 139 us with a block too many for each item, 94 without).  A unit has an
+  // item for each row tile (pair 2) or for each two (pair 1) of a sequence.  Splits add at most
+  // work / c: with C = work / SMs, c is at least C up to kPkFine, and at least kPkFine and C / 3
+  // above it.
+  const int64_t rows = p.pair == 2 ? p.TQ : 2 * p.TQ, tiles = p.Tq / rows + std::min(p.n, p.Tq);
+  const int64_t all = (p.Tq + rows - 1) / rows, prefix = p.Lp ? all : 0;
+  const int64_t work = p.units * all * (p.Tk / lx::kPkKeys + p.n + (p.Lp + lx::kPkKeys - 1) / lx::kPkKeys);
+  const int64_t splits = !p.part ? 0 : std::min({work, std::max<int64_t>(lx::kPkSMs, work / lx::kPkFine), (int64_t)3 * lx::kPkSMs});
+  const int64_t items = splits + (tiles + prefix) * p.units, blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
   if (items > 0x7FFFFFFE || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(lx::packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)

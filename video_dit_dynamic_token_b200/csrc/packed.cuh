@@ -1012,30 +1012,49 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
   const int np = p.Lp ? pack_splits(p, rows, pack_tiles(p.Lp), c, p.max_np) : 0;
   const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
   if (!p.Lp && ns == 1) return;   // its item finished the row
-  float m = -INFINITY;
-  for (int i = lane; i < np + ns; i += 32) m = fmaxf(m, p.ml[i * R + row].x);
-#pragma unroll
-  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  const float at = m == -INFINITY ? 0.f : m;
-  float o[E], l = 0.f;
+  float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < np + ns; ++i) {
-    const float2 x = p.ml[i * R + row];
-    const float w = ex2f(x.x - at);
-    l = fmaf(w, x.y, l);
-    const float* src = p.part + (i * R + row) * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(src);
-      o[0] = fmaf(w, y.x, o[0]);
-      o[1] = fmaf(w, y.y, o[1]);
-      o[2] = fmaf(w, y.z, o[2]);
-      o[3] = fmaf(w, y.w, o[3]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      o[0] = fmaf(w, y.x, o[0]);
-      o[1] = fmaf(w, y.y, o[1]);
+  // 32 splits at a time, a weight in each lane; the rows of 8 are on their way together, with
+  // the maxima and sums (one after another: 10.8 us instead of 8.3 for 2,560 rows of 12 splits)
+  for (int b = 0; b < np + ns; b += 32) {
+    const int count = min(32, np + ns - b);
+    const long long base = (long long)b * R + row;
+    const float2 x = lane < count ? p.ml[base + lane * R] : make_float2(-INFINITY, 0.f);
+    float w = 0.f;
+    for (int i = 0; i < count; i += 8) {
+      float y[8][E];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* src = p.part + (base + (i + u) * R) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 z = i + u < count ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+          y[u][0] = z.x, y[u][1] = z.y, y[u][2] = z.z, y[u][3] = z.w;
+        } else {
+          const float2 z = i + u < count ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+          y[u][0] = z.x, y[u][1] = z.y;
+        }
+      }
+      if (i == 0) {
+        float top = fmaxf(m, x.x);
+#pragma unroll
+        for (int v = 16; v; v >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, v));
+        const float at = top == -INFINITY ? 0.f : top, a = ex2f(m - at);   // 0 from -inf
+        w = ex2f(x.x - at);
+        float sum = w * x.y;
+#pragma unroll
+        for (int v = 16; v; v >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, v);
+        l = fmaf(l, a, sum);
+        m = top;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= a;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, (i + u) & 31);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(wu, y[u][e], o[e]);
+      }
     }
   }
   const int seen = p.causal ? max(0, min(s.lk, tok - s.q0 + s.lk - s.lq + 1)) : s.lk;

@@ -37,10 +37,12 @@
 // of the first half of P(j) with V, that of the second half, S(j+1): the first product
 // runs under the second half's exponentials, S(j+1) may overwrite P(j) because the tensor
 // core runs a thread's MMAs in order, and its commit also says that O has P(j) V(j), so
-// the softmax may rescale O without another barrier.  (Half tiles with two score
-// buffers, which take the scores out of the stream's chain, were slower: 12.1 against
-// 10.4 ms for the 480p grid, a 64-column MMA reading Q twice as often and every half paying
-// for its own hand-over.)
+// the softmax may rescale O without another barrier.  What bounds a long row: a stream's chain
+// of 3,500 clocks per tile (scores to P 2,300, of which the exponentials 1,600; P to scores
+// 1,000), two of which overlap; its MMAs take 1,024.  Measured and slower for the 480p grid (9.9
+// ms): half tiles with two score buffers 12.1; the first half of S(j+1) issued between the
+// halves of P V 10.7 (64-column MMAs take 1.5 times as long per column, Q being read twice as
+// often); 16 softmax warps 11.3 and more.
 //
 // The reference that the exponents are taken against is not the running maximum but
 // follows it: it moves only when the maximum of a tile has passed it by more than 2^8, so
@@ -459,6 +461,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       bar_pfull[NQ][2], bar_odone[NQ], bar_ifull[kPkItems], bar_iempty[kPkItems], bar_clc, bar_drain[NQ];
   __shared__ __align__(16) uint4 clc;
   __shared__ uint32_t tmem_slot;
+  __shared__ volatile int busy[NQ][4];   // a warp is at its exponentials
   __shared__ volatile int abort_flag;
   __shared__ int never_abort;
   __shared__ PackTable table;
@@ -486,6 +489,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     for (int g = 0; g < NQ; ++g) mbar_init(&bar_drain[g], 1);
     abort_flag = 0;
     never_abort = 0;
+    for (int i = 0; i < 8; ++i) busy[i >> 2][i & 3] = 0;
     fence_barrier_init();
   }
   // the work ahead of this kernel may still run up to here
@@ -777,8 +781,13 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         if (j * kPkKeys + kPkKeys > whole) {              // some row does not see all of this tile
           const int nv = ahead - j * kPkKeys;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= nv) sv[c] = 0xFF800000u;             // -inf
+          for (int b = 0; b < kPkKeys; b += kPkHalf) {
+            if (b + kPkHalf + j * kPkKeys > whole) {
+#pragma unroll
+              for (int c = b; c < b + kPkHalf; ++c)
+                if (c >= nv) sv[c] = 0xFF800000u;         // -inf
+            }
+          }
         }
         const float* f = reinterpret_cast<const float*>(sv);
         auto maximum = [&]() {
@@ -829,7 +838,9 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
             const int c = from + 2 * i;
             float x0, x1;
             f2unpack(fma2(f2pack(f[c], f[c + 1]), sc2, nm2), x0, x1);
-            const float p0 = ex2f(x0), p1 = ex2f(x1);
+            float p0, p1;                      // in this order (reordered by the compiler: 2 % slower)
+            asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(x0));
+            asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(x1));
             sum2[i & 3] = add2(sum2[i & 3], f2pack(p0, p1));
             const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
             pk[(c & 63) >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
@@ -837,6 +848,12 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         };
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum2[i] = 0;
+        // The two warps of a scheduler (one of each stream) take turns with their exponentials: both
+        // at once leave the special function unit idle while both wait for their MMAs (480p grid
+        // 10.5 ms without, 9.9 with).  Nothing depends on it: after 100 looks, longer than a turn of
+        // 1,600 clocks, or where both look at once, they go ahead together.
+        for (int spin = 0; spin < 100 && busy[1 - g][quarter]; ++spin) {}
+        if (lane == 0) busy[g][quarter] = 1;
         exponentials(0, 32);
         tmem_st32(s_addr, pk);
         if (two) {
@@ -849,6 +866,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           exponentials(80, 24);
           tmem_st32(s_addr + 64, pk);
         }
+        if (lane == 0) busy[g][quarter] = 0;
         float a0, a1, b0, b1;
         f2unpack(add2(sum2[0], sum2[1]), a0, a1);
         f2unpack(add2(sum2[2], sum2[3]), b0, b1);

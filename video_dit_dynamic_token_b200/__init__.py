@@ -26,7 +26,7 @@ from functools import lru_cache
 import torch
 
 from . import _abi
-from ._abi import LX_BLOCK, LX_MODE_BF16, LX_MODE_INT8FP8, LxBhld, LxPlan  # noqa: F401
+from ._abi import LX_BLOCK, LX_MODE_BF16, LX_MODE_INT8FP8, LxBhld, LxPack, LxPlan  # noqa: F401
 
 MODES = {"bf16": LX_MODE_BF16, "int8fp8": LX_MODE_INT8FP8}
 
@@ -398,10 +398,13 @@ def _with_stream(stream, t, call):
         return call()
 
 
-def _same_device(*tensors):
-    """The device index of CUDA tensors that are all on one device (None entries are skipped)."""
+def _same_device(tensors, optional=()):
+    """The device index of CUDA tensors that are all on one device (those that are None are skipped)."""
     d = tensors[0].get_device()
     for t in tensors:
+        if t.get_device() != d:
+            raise ValueError("tensors are on different devices")
+    for t in optional:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors are on different devices")
     if d < 0:
@@ -444,30 +447,34 @@ def _attn_packed(prefix, Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws
                                                             lse, ws, None))
     if out is None:
         out = torch.empty_like(Q)
-    dev = _same_device(Q, K, V, out, cu_q, cu_k, len_k, lse, ws, *prefix)
+    dev = _same_device((Q, K, V, out, cu_q, cu_k), (len_k, lse, ws, *prefix))
     if dev != _current_device():
         with torch.cuda.device(dev):
             return _attn_packed(prefix, Q, K, V, cu_q, cu_k, causal, scale, len_k, out, lse, ws, None)
-    n = cu_q.numel() - 1
-    for t, shape in ((cu_q, (n + 1,)), (cu_k, (n + 1,)), (len_k, (n,))):
-        if t is not None and (t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous()):
-            raise ValueError("cu_q and cu_k: contiguous int32 tensors of n + 1 entries, len_k of n")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != Q.shape[1:3] or not lse.is_contiguous()):
+    starts = cu_q.shape
+    n = starts[0] - 1 if len(starts) == 1 else -1
+    if (cu_k.shape != starts or cu_q.dtype is not torch.int32 or cu_k.dtype is not torch.int32 or n < 0
+            or not cu_q.is_contiguous() or not cu_k.is_contiguous()
+            or len_k is not None and (len_k.dtype is not torch.int32 or len_k.shape != (n,) or not len_k.is_contiguous())):
+        raise ValueError("cu_q and cu_k: contiguous int32 tensors of n + 1 entries, len_k of n")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != Q.shape[1:3] or not lse.is_contiguous()):
         raise ValueError("lse: a contiguous fp32 [Hq, Tq] tensor")
     q, k, v, o = bhld(Q), bhld(K), bhld(V), bhld(out)
+    D = q.D
     if ws is None:
-        size = _prefix_ws(q.H, q.L, q.D) if prefix else _packed_ws(q.H, q.L, k.H, k.L, q.D, n)
-        ws = Q.new_empty(size, dtype=torch.uint8) if size else None
-    ref = ctypes.byref
-    pk = _abi.LxPack(cu_q.data_ptr(), cu_k.data_ptr(), len_k.data_ptr() if len_k is not None else None, n)
-    tail = (ref(k), ref(v), ref(pk), 1 if causal else 0, q.D ** -0.5 if scale is None else scale, ref(o),
-            lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None,
-            ws.numel() * ws.element_size() if ws is not None else 0, _raw_stream(dev))
-    if prefix:
-        kp, vp = bhld(prefix[0]), bhld(prefix[1])
-        _check(_abi.load().lx_attn_prefix(ref(q), ref(kp), ref(vp), *tail), "lx_attn_prefix")
+        size = _prefix_ws(q.H, q.L, D) if prefix else _packed_ws(q.H, q.L, k.H, k.L, D, n)
+        if size:
+            ws = Q.new_empty(size, dtype=torch.uint8)
+    pk = LxPack(cu_q.data_ptr(), cu_k.data_ptr(), None if len_k is None else len_k.data_ptr(), n)
+    tail = (k, v, pk, 1 if causal else 0, D ** -0.5 if scale is None else scale, o,
+            None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(dev))
+    if prefix:   # (ctypes passes a structure's address where a pointer to it is declared)
+        status = _abi.load().lx_attn_prefix(q, bhld(prefix[0]), bhld(prefix[1]), *tail)
     else:
-        _check(_abi.load().lx_attn_packed(ref(q), *tail), "lx_attn_packed")
+        status = _abi.load().lx_attn_packed(q, *tail)
+    if status:
+        _check(status, "lx_attn_prefix" if prefix else "lx_attn_packed")
     return out
 
 
@@ -548,34 +555,38 @@ def lx_nvfp4_gemv_ws_size(M, K) -> int:
 
 def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None):
     """Y = x W^T + bias in bf16 [M, N] for M <= 16 bf16 rows x [M, K] and NVFP4 W [N, K]; bias fp32 [N] or None."""
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("expected a bf16 [M, K] tensor with contiguous rows")
     if stream is not None:
         return _with_stream(stream, x, lambda: lx_nvfp4_gemv(x, wq, bias, out, ws))
+    strides = x.stride()
+    if x.dtype is not torch.bfloat16 or len(strides) != 2 or strides[1] != 1:
+        raise ValueError("expected a bf16 [M, K] tensor with contiguous rows")
     M, K = x.shape
-    N = wq.R
+    N, codes, sf, gw = wq.R, wq.codes, wq.sf, wq.gscale
     if K != wq.K:
         raise ValueError("x and W differ in K")
-    if wq.codes.numel() * 2 != N * K or wq.sf.numel() < (N + 127) // 128 * 8 * K:
+    if codes.numel() * 2 != N * K or sf.numel() < (N + 127) // 128 * 8 * K:
         raise ValueError("W: not the codes and scales of an [N, K] tensor")
-    if out is None:
-        out = x.new_empty((M, N))
-    elif out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
-        raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
-    if bias is not None and (bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != N):
+    if bias is not None and (bias.dtype is not torch.float32 or not bias.is_contiguous() or bias.numel() != N):
         raise ValueError("bias must be a contiguous fp32 tensor of N elements")
-    dev = _same_device(x, out, wq.codes, wq.sf, wq.gscale, bias, ws)
+    dev = _same_device((x, codes, sf, gw), (bias, out, ws))
     if dev != _current_device():
         with torch.cuda.device(dev):
             return lx_nvfp4_gemv(x, wq, bias, out, ws)
+    if out is None:
+        out = x.new_empty((M, N))
+        ldy = N
+    elif out.dtype is torch.bfloat16 and out.shape == (M, N) and out.stride(1) == 1:
+        ldy = out.stride(0) if M > 1 else max(out.stride(0), N)
+    else:
+        raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
     if ws is None:
         ws = x.new_empty(lx_nvfp4_gemv_ws_size(M, K), dtype=torch.uint8)
-    ldx = x.stride(0) if M > 1 else max(x.stride(0), K)
-    ldy = out.stride(0) if M > 1 else max(out.stride(0), N)
-    _check(_abi.load().lx_nvfp4_gemv(x.data_ptr(), M, ldx, wq.codes.data_ptr(), wq.sf.data_ptr(), wq.gscale.data_ptr(),
-                                     bias.data_ptr() if bias is not None else None, N, K, out.data_ptr(), ldy,
-                                     ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev)),
-           "lx_nvfp4_gemv")
+    status = _abi.load().lx_nvfp4_gemv(
+        x.data_ptr(), M, strides[0] if M > 1 else max(strides[0], K), codes.data_ptr(), sf.data_ptr(), gw.data_ptr(),
+        None if bias is None else bias.data_ptr(), N, K, out.data_ptr(), ldy, ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(dev))
+    if status:
+        _check(status, "lx_nvfp4_gemv")
     return out
 
 

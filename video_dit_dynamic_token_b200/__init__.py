@@ -11,9 +11,11 @@ the quantisers (lx_quantize_qk, lx_pool_quantize_qk, lx_quantize_v), the
 attention (lx_attn_bf16, lx_attn_int8fp8, lx_sparse_attn_fwd), plan and
 forward in one call (lx_sparse_attn), the fused Q/K prologue (lx_rope3d_table,
 lx_qk_prologue), K smoothing (lx_k_channel_mean, lx_quantize_qk_smooth,
-lx_pool_quantize_qk_smooth), NVFP4 (lx_nvfp4_quantize, lx_nvfp4_gemm); the
-host-to-host pipeline is in ``pipeline`` and the Light-Ulysses exchange in
-``ulysses``.
+lx_pool_quantize_qk_smooth), NVFP4 (lx_nvfp4_quantize, lx_nvfp4_gemm, and
+lx_nvfp4_gemv for few bf16 rows), dense attention over packed sequences
+(lx_attn_packed: prompts, cross-attention, single tokens over a cache) and
+behind a shared prefix (lx_attn_prefix); the host-to-host pipeline is in
+``pipeline`` and the Light-Ulysses exchange in ``ulysses``.
 """
 from __future__ import annotations
 

@@ -261,3 +261,49 @@ def test_wrappers_refuse(lx, layer):
     with pytest.raises(lx.LxError):
         lx.lx_nvfp4_gemv(_rand(gen, 17, HID), layer.o)
     assert lx.lx_last_device_status() == 0
+
+
+def test_captured_between_streams(lx, layer):
+    """A captured call behind a copy, behind work of two streams, and in front of work on another one."""
+    gen = torch.Generator().manual_seed(15)
+    n = 3
+    x, x2 = _rand(gen, n, HID), _rand(gen, n, HID)
+    q, k, v = _rand(gen, 1, HQ, n, D), _rand(gen, 1, HKV, n * 600, D), _rand(gen, 1, HKV, n * 600, D)
+    cq, ck = _i32(range(n + 1)), _i32(600 * i for i in range(n + 1))
+    kc, xc = torch.zeros_like(k), torch.zeros_like(x)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        kc.copy_(k)                                       # a copy in front
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            xc.copy_(x)
+            a = lx.lx_nvfp4_gemv(xc, layer.qkv, bias=layer.qkv_bias)
+        b = lx.lx_attn_packed(q, kc, v, cq, ck)
+        main.wait_stream(side)                            # two streams in front
+        c = lx.lx_attn_prefix(q, kc, v, kc, v, cq, ck)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):                     # on another stream behind
+            d = lx.lx_nvfp4_gemv(x2, layer.qkv, bias=layer.qkv_bias)
+            e = lx.lx_attn_packed(c, kc, v, cq, ck)
+        main.wait_stream(side)
+        return a, b, c, d, e
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        want = work()
+    main.synchronize()
+    assert lx.lx_last_device_status() == 0
+    plain = lx.lx_attn_packed(want[2], k, v, cq, ck)
+    assert torch.equal(plain, want[4])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        got = work()
+    for _ in range(3):
+        for t in (*got, kc, xc):
+            t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert lx.lx_last_device_status() == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -433,18 +433,39 @@ __device__ __noinline__ void packed_exact_row(const __nv_bfloat16* q, const __nv
   }
   m = -INFINITY;
   l = 0.f;
-  for (int u = lo; u < hi; ++u) {
-    float s = 0.f;
+  constexpr int N = 4;   // keys at a time, whose loads and sums overlap
+  for (int u = lo; u < hi; u += N) {
+    float s[N], vf[N][E], mn = m;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qf[e], __bfloat162float(k[u * ksL + lane * E + e]), s);
+    for (int i = 0; i < N; ++i) {
+      s[i] = 0.f;
 #pragma unroll
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= scale_log2;
-    const float mn = fmaxf(m, s), at = mn == -INFINITY ? 0.f : mn;
-    const float a = m == -INFINITY ? 0.f : ex2f(m - at), x = ex2f(s - at);
-    l = fmaf(l, a, x);
+      for (int e = 0; e < E; ++e) {
+        const bool in = u + i < hi;
+        s[i] = fmaf(qf[e], in ? __bfloat162float(k[(u + i) * ksL + lane * E + e]) : 0.f, s[i]);
+        vf[i][e] = in ? __bfloat162float(v[(u + i) * vsL + lane * E + e]) : 0.f;
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(x, __bfloat162float(v[u * vsL + lane * E + e]), o[e] * a);
+    for (int w = 16; w; w >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s[i] = u + i < hi ? s[i] * scale_log2 : -INFINITY;
+      mn = fmaxf(mn, s[i]);
+    }
+    const float at = mn == -INFINITY ? 0.f : mn, a = m == -INFINITY ? 0.f : ex2f(m - at);
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= a;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = ex2f(s[i] - at);
+      l += x;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(x, vf[i][e], o[e]);
+    }
     m = mn;
   }
 }
@@ -954,6 +975,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       }
       // rows that a hidden key's non-finite V may have spoilt
       uint32_t redo = __ballot_sync(0xffffffffu, any && check != check && seen < to);
+      if (redo) __syncwarp();   // the rows' own stores come first
       while (redo) {
         const int src = __ffs(redo) - 1;
         redo &= redo - 1;

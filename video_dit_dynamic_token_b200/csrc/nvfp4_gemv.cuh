@@ -5,9 +5,9 @@
 // for M <= 16 rows, x kept in bf16 precision (the modulation vectors of a
 // timestep, a guided pair, single new tokens).  The weights are read once: N K / 2
 // bytes of codes and N K / 16 of scales, which is what bounds large ones (30720 x 5120, cold:
-// one row 21.5 us = 4.1 TB/s, 120 of the 148 SMs having a tile; 8 rows 24.8, 16 rows 26.3).
+// one row 21.5 us = 4.1 TB/s, 120 of the 148 SMs having a tile; 8 and 16 rows 23.3).
 // Small ones are bound by the start of two kernels and the joining of sums (5120 x 5120, two
-// rows: 9.2 us; 256 x 512, one row: 5.6).
+// rows: 8.5 us; 256 x 512, one row: 5.7).
 //
 // Decoding 4-bit weights costs more issue slots than an SM has at the rate they
 // arrive (42 weights per clock; mma.sync on weights decoded to fp16 took 38 to 55 us
@@ -180,6 +180,15 @@ __global__ void __launch_bounds__(128) nvfp4_gemv_digits_kernel(const __nv_bfloa
     *reinterpret_cast<uint32_t*>(codes + (long long)(m * P + d) * (K / 2) + k / 2) = word[d];
 }
 
+__device__ __forceinline__ void mma_nvf4_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};"
+      "\n\ttcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], da, db, %4, [%6], [%7], p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -188,10 +197,11 @@ __device__ __forceinline__ void cluster_sync() {
 // K; one CTA per SM.  Stages of 256 codes go through a ring:
 //   warp 0: loads; those of the weights do not wait for the digit pass;
 //   warp 1: MMAs;
-//   warps 2 .. 5: move each stage's scales from shared memory to TMEM (a row of the
-//           tiled layout per lane, the same in all four lane quarters), then the
-//           sums.  tcgen05.cp does the same in the tensor pipe, where each copy of 512
-//           bytes took 70 clocks between MMAs of 128.
+//   warps 2 .. 9: two sets in turn move a stage's scales from shared memory to TMEM (a row
+//           of the tiled layout per lane, the same in all four lane quarters), then the
+//           sums.  One set takes 1,000 clocks a stage, whose MMAs take 420.  tcgen05.cp
+//           does the same in the tensor pipe, where each copy of 512 bytes took 70
+//           clocks between MMAs of 105.
 // All ten warps then turn digit sums into outputs.  The digits' own scales are 1.  (Digits
 // made by warps of this kernel, stage by stage, were no faster for one row and cost
 // up to 40 us more for 16, every CTA reading its part of x twice.)  The CTAs of a cluster split K and add their sums over
@@ -245,6 +255,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = tmem_slot;
+  int info = 0;                                              // of row `lane` of x
 
   if (warp == 0) {
     if (lane == 0) {
@@ -287,19 +298,28 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
   } else if (warp == 1) {
     if (lane == 0) {
       // ================= MMA =================
+      // One thread issues them all, so its instructions per stage count: descriptors as low words
+      // (the high word is common), slot and phase kept as they go (1,000 clocks a stage without
+      // that, 850 with it; the MMAs take 450)
+      const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, SW_128B);
+      const uint32_t hi = (uint32_t)(d0 >> 32);
+      const int last = KS - 4 * (kb0 + n - 1);       // k-steps of the last stage, if fewer than 4
       bool ok = true;
+      uint32_t ph = 0;
+      int s = 0;
       for (int i = 0; i < n; ++i) {
-        const int s = i % stages, steps = min(4, KS - 4 * (kb0 + i));
-        const uint32_t ph = (uint32_t)(i / stages) & 1u;
         ok = mbar_wait(&bar_full[s], ph, &abort_flag, a.limit_ns) && mbar_wait(&bar_sf[s], ph, &abort_flag, a.limit_ns);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(sm + s * stage_bytes), xt = st + kGvBBytes + kGvSfBytes;
-        const uint32_t tsf = tb + 288u + (uint32_t)s * 32u;
-        for (int kk = 0; kk < steps; ++kk)
-          mma_nvf4(tb, smem_desc(xt + kk * 32u, 16, 1024, SW_128B), smem_desc(st + kk * 32u, 16, 1024, SW_128B), kNvIdesc,
-                   tb + 256u, tsf + kk * 8u, (i | kk) != 0 ? 1u : 0u);
+        const uint32_t wlo = (uint32_t)d0 + s * (stage_bytes >> 4), xlo = wlo + ((kGvBBytes + kGvSfBytes) >> 4);
+        const uint32_t tsf = tb + 288u + 32u * s;
+        const int steps = i + 1 < n ? 4 : last;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < steps)
+            mma_nvf4_lo(tb, xlo + 2u * kk, wlo + 2u * kk, hi, kNvIdesc, tb + 256u, tsf + kk * 8u, (i | kk) != 0 ? 1u : 0u);
         mma_commit(&bar_empty[s]);
+        if (++s == stages) s = 0, ph ^= 1u;
       }
       if (ok) mma_commit(&bar_acc);
       if (!ok) {
@@ -311,21 +331,27 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
       mbar_wait(&bar_drain, 0, &never_abort, a.limit_ns);
     }
     __syncwarp();
-  } else if (warp < 6) {
-    // ================= scales to TMEM =================
-    const int quarter = warp & 3;
+  } else {
+    // ================= scales to TMEM: stages in turn =================
+    const int quarter = warp & 3, set = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    {
+    asm volatile("griddepcontrol.wait;" ::: "memory");                 // the digits and exponents are complete
+    info = a.ref[min(lane, M - 1)];
+    if (set == 0) {
       uint32_t one[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) one[i] = 0x38383838u;               // E4M3 1.0
       tmem_st16(tb + lanes + 256u, one);
     }
     bool ok = true;
+    int slot = stages - 1;
+    uint32_t ph = 1;
     for (int i = 0; i < n; ++i) {
-      const int s = i % stages, steps = min(4, KS - 4 * (kb0 + i));
-      ok = warp_wait(&bar_full[s], (uint32_t)(i / stages) & 1u, &abort_flag, a.limit_ns);
+      if (++slot == stages) slot = 0, ph ^= 1u;
+      const int s = slot, steps = min(4, KS - 4 * (kb0 + i));
+      ok = warp_wait(&bar_full[s], ph, &abort_flag, a.limit_ns);
       if (!ok) break;
+      if ((i & 1) != set) continue;   // the other set's; waited for all the same, as phases alternate
       const uint4* sf = reinterpret_cast<const uint4*>(sm + s * stage_bytes + kGvBBytes) + lane;
       uint32_t v[32];
 #pragma unroll
@@ -354,7 +380,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
     tc_fence_after();
     if (ok && quarter * 32 < rows) {
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 64) {
+      for (int c = 128 * set; c < 128 * set + 128; c += 64) {
         uint32_t v[2][32];
         tmem_ld32(tb + lanes + (uint32_t)c, v[0]);
         tmem_ld32(tb + lanes + (uint32_t)c + 32u, v[1]);
@@ -379,25 +405,42 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
     tc_fence_after();
     tmem_dealloc(tb, kGvTmemCols);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int o = threadIdx.x; o < M * 256; o += kGvThreads) {
-    const int m = o >> 8, col = o & 255, info = a.ref[m], e = (info & 0xFFFF) - 127;
-    float v = 0.f;
+  if (warp >= 2) {
+    // four columns of every fourth row of x a thread
+    const int col = 4 * ((threadIdx.x - 64) & 63);
+    for (int m = (threadIdx.x - 64) >> 6; m < M; m += 4) {
+      const int f = __shfl_sync(0xffffffffu, info, m), e = (f & 0xFFFF) - 127;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int h = 0; h < P / 8; ++h) {   // the low digits first
-      float u = 0.f;
+      for (int h = 0; h < P / 8; ++h) {   // the low digits first
+        const float* row = dsum + (m * P + 8 * h) * 256;
+        float4 x[8];                      // digit d (row 8 i + d): piece (col / 4) ^ d of its row
 #pragma unroll
-      for (int d = 7; d >= 0; --d) {
-        const int r = m * P + 8 * h + d;
-        u = fmaf(u, 8.f, dsum[r * 256 + (((col >> 2) ^ (r & 7)) << 2) + (col & 3)]);
+        for (int d = 0; d < 8; ++d) x[d] = *reinterpret_cast<const float4*>(row + d * 256 + (((col >> 2) ^ d) << 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u = 0.f;
+#pragma unroll
+          for (int d = 7; d >= 0; --d) u = fmaf(u, 8.f, i == 0 ? x[d].x : i == 1 ? x[d].y : i == 2 ? x[d].z : x[d].w);
+          v[i] = fmaf(v[i], 0x1p-21f, u);
+        }
       }
-      v = fmaf(v, 0x1p-21f, u);
+      const float a1 = pow2f(e >> 1), a2 = pow2f(e - (e >> 1) - 21);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * a1 * a2;
+      *reinterpret_cast<float4*>(part + m * 256 + col) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    v = v * pow2f(e >> 1) * pow2f(e - (e >> 1) - 21);
-    const long long nr = (long long)tile * 256 + col;
-    if ((info & kGvBadRow) && nr < a.N) {
+    if (__any_sync(0xffffffffu, lane < M && (info & kGvBadRow)))   // (the same for all warps)
+      asm volatile("bar.sync 1, 256;" ::: "memory");               // a thread reads what its neighbours wrote
+    // elements of x that are not finite: their products, one by one
+    for (uint32_t bad = __ballot_sync(0xffffffffu, lane < M && (info & kGvBadRow)); bad; bad &= bad - 1) {
+      const int m = __ffs(bad) - 1;
+      const int col = threadIdx.x - 64;
+      const long long nr = (long long)tile * 256 + col;
+      if (nr >= a.N) continue;
       const int end = min((kb0 + n) * 256, a.K), row = col & 127;
       const uint8_t* sf = a.wsf + (nr / 128) * KS * 512 + (row % 32) * 16 + (row / 32) * 4;
+      float v = part[m * 256 + col];
       for (int k = kb0 * 256; k < end; ++k) {
         const float xv = __bfloat162float(a.x[m * a.ldx + k]);
         if (fabsf(xv) < INFINITY) continue;
@@ -406,28 +449,39 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
         wv *= e4m3_to_f32(sf[(k / 64) * 512 + (k / 16) % 4]);
         v = fmaf(xv, (c & 8u) ? -wv : wv, v);
       }
+      part[m * 256 + col] = v;
     }
-    part[o] = v;
   }
-  // every CTA of the cluster adds a share of the outputs, in rank order
+  // every CTA of the cluster adds a share of the outputs, four at a time, in rank order
   cluster_sync();
   const float gw = *a.gw;
   const uint32_t base = smem_u32(part);
-  for (int o = (int)(rank * kGvThreads + threadIdx.x); o < M * 256; o += (int)ranks * kGvThreads) {
-    const int m = o >> 8;
-    const long long nr = (long long)tile * 256 + (o & 255);
-    float v[kGvSplit];
+  for (int o = (int)(rank * kGvThreads + threadIdx.x); o < M * 64; o += (int)ranks * kGvThreads) {
+    float4 v[kGvSplit];
 #pragma unroll
     for (uint32_t r = 0; r < kGvSplit; ++r) {
+      if (r >= ranks) break;
       uint32_t at;
-      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 4u * (uint32_t)o), "r"(min(r, ranks - 1)));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(at) : "memory");
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 16u * (uint32_t)o), "r"(r));
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                   : "r"(at)
+                   : "memory");
     }
-    float s = v[0];
+    float s[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-    for (uint32_t r = 1; r < kGvSplit; ++r)
-      if (r < ranks) s += v[r];
-    if (nr < a.N) a.y[m * a.ldy + nr] = __float2bfloat16(__fadd_rn(__fmul_rn(s, gw), a.bias ? a.bias[nr] : 0.f));
+    for (uint32_t r = 1; r < kGvSplit; ++r) {
+      if (r >= ranks) break;
+      s[0] += v[r].x;
+      s[1] += v[r].y;
+      s[2] += v[r].z;
+      s[3] += v[r].w;
+    }
+    const long long first = (long long)tile * 256 + 4 * (o & 63);
+    __nv_bfloat16* y = a.y + (o >> 6) * a.ldy + first;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (first + i < a.N) y[i] = __float2bfloat16(__fadd_rn(__fmul_rn(s[i], gw), a.bias ? a.bias[first + i] : 0.f));
   }
   // no CTA leaves while another may still read its sums
   cluster_sync();

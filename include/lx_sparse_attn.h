@@ -315,7 +315,7 @@ typedef struct lx_pack {
   const int32_t* cu_q;  /* device [n + 1], ascending, within Q's rows */
   const int32_t* cu_k;  /* device [n + 1], ascending, within K's rows */
   const int32_t* len_k; /* device [n], 0 <= len_k[i] <= cu_k[i+1] - cu_k[i], or NULL */
-  int64_t n;            /* sequences, >= 1 */
+  int64_t n;            /* sequences, 1 .. 2^20 */
 } lx_pack;
 
 /* Workspace of lx_attn_packed: 0 for prompts that fill the GPU without splitting
@@ -388,8 +388,9 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
                         const uint8_t* wsf, const float* gw, const float* bias, int64_t M, int64_t N, int64_t K,
                         void* y, int64_t ldy, cudaStream_t stream);
 
-/* Workspace of lx_nvfp4_gemv. */
-lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t K, size_t* bytes);
+/* Workspace of lx_nvfp4_gemv for x [M, K] and W [N, K]; 0 for up to 8 rows of together at
+ * most 10240 elements and at most 2^25 weights. */
+lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
 
 /* Y[m, n] = bf16(fl32(acc[m, n] * gw) + bias[n]) for M <= 16 bf16 rows x [M, K] (row
  * stride ldx elements, ldx % 8 == 0) that are not quantised: timestep modulation,
@@ -400,8 +401,8 @@ lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t K, size_t* bytes);
  * 2^-22.
  * W = (wc, wsf, gw) [N, K] as written by lx_nvfp4_quantize, N at most 2^30, K % 64 == 0
  * and at most 2^24; bias fp32 [N] or NULL; y bf16 [M, N], row stride ldy >= N.  x, wc, wsf
- * 16-byte aligned; ws of the size above, 256-byte aligned, not shared by calls that may
- * overlap.  More rows are LX_ERR_UNSUPPORTED: lx_nvfp4_gemm is the form for them. */
+ * 16-byte aligned; ws of the size above, 256-byte aligned (may be NULL for size 0), not
+ * shared by calls that may overlap.  More rows are LX_ERR_UNSUPPORTED: lx_nvfp4_gemm is the form for them. */
 lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc, const uint8_t* wsf, const float* gw,
                         const float* bias, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, size_t ws_bytes,
                         cudaStream_t stream);

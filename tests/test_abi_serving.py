@@ -111,9 +111,13 @@ def test_gemv_refusals(lib):
     assert call(g=g + 2) == ALI and call(b=0x60002) == ALI and call(y=y + 1) == ALI
     assert call(K=(1 << 24) + 64, ldx=(1 << 24) + 64) == UNS
     n = ctypes.c_size_t()
-    size = lambda M, K: lib.lx_nvfp4_gemv_ws_size(M, K, ctypes.byref(n))
-    assert size(3, 320) == 0 and n.value == 3 * 16 * 160 + 256       # 16 digits for up to 8 rows
-    assert call(M=3, K=320, ldx=320, wb=n.value - 1) == WSP and call(ws=None) == WSP and call(ws=0x70010) == ALI
+    size = lambda M, K, N=100: lib.lx_nvfp4_gemv_ws_size(M, N, K, ctypes.byref(n))
+    assert size(3, 320) == 0 and n.value == 0 and size(8, 1280) == 0 and n.value == 0   # digits in the product kernel
+    assert size(2, 5120, 6553) == 0 and n.value == 0 and size(2, 5120, 6554) == 0 and n.value == 2 * 16 * 2560 + 256
+    assert size(8, 1344) == 0 and n.value == 8 * 16 * 672 + 256      # 16 digits for up to 8 rows
+    big = dict(M=8, K=1344, ldx=1344)
+    assert call(**big, wb=n.value - 1) == WSP and call(**big, ws=None) == WSP and call(**big, ws=0x70010) == ALI
     assert size(9, 320) == 0 and n.value == 9 * 8 * 160 + 256        # 11520 is a multiple of 256
-    assert size(17, 320) == UNS and size(1, (1 << 24) + 64) == UNS
-    assert size(1, 100) == INV and size(0, 64) == INV and lib.lx_nvfp4_gemv_ws_size(1, 64, None) == INV
+    assert size(17, 320) == UNS and size(1, (1 << 24) + 64) == UNS and size(1, 64, (1 << 30) + 1) == UNS
+    assert size(1, 100) == INV and size(0, 64) == INV and size(1, 64, 0) == INV
+    assert lib.lx_nvfp4_gemv_ws_size(1, 64, 64, None) == INV

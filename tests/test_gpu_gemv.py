@@ -217,3 +217,23 @@ def test_capture_streams_and_repeatability(lx):
     torch.cuda.synchronize()
     ref = _ref(x.float().cpu().numpy(), wr)
     assert np.all(np.abs(out.float().cpu().numpy() - ref["y"]) <= _bound(ref, 1024))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 10240), (1, 300, 10304), (8, 300, 1280), (8, 300, 1344), (7, 513, 1408),
+                                   (3, 40, 64), (5, 9000, 2048), (2, 6553, 5120), (2, 6554, 5120)])
+def test_digits_in_the_product_kernel_and_before_it(lx, M, N, K):
+    """Both sides of the rule for where digits are made; then rows that hold infinities and NaN."""
+    rng = np.random.default_rng(M + N + K)
+    wq, wr = _weights(lx, rng, N, K)
+    x = _bf16(rng.standard_normal((M, K)) * 2.0 ** rng.integers(-20, 20, (M, 1)))
+    bias = rng.standard_normal(N).astype(np.float32)
+    y = _check(lx, x, wq, wr, bias)
+    assert (lx.lx_nvfp4_gemv_ws_size(M, N, K) == 0) == (M * K <= 10240 and N * K <= 2 ** 25)
+    spoilt = x.clone()
+    spoilt[0, K - 1] = float("inf")
+    z = lx.lx_nvfp4_gemv(spoilt, wq, torch.from_numpy(bias).to(DEV))
+    assert lx.lx_last_device_status() == 0
+    w = oracle.dequant_nvfp4_ref(wr["codes"], wr["sf"], wr["g"])[:, K - 1]
+    got = z[0].float().cpu().numpy()
+    assert np.all(got[w > 0] == np.inf) and np.all(got[w < 0] == -np.inf) and np.all(np.isnan(got[w == 0]))
+    assert torch.equal(z[1:], y[1:])

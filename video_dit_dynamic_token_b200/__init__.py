@@ -549,9 +549,9 @@ def lx_nvfp4_gemm(xq: NvFp4Tensor, wq: NvFp4Tensor, bias=None, out=None, stream=
 
 
 @lru_cache(maxsize=4096)
-def lx_nvfp4_gemv_ws_size(M, K) -> int:
+def lx_nvfp4_gemv_ws_size(M, N, K) -> int:
     b = ctypes.c_size_t()
-    _check(_abi.load().lx_nvfp4_gemv_ws_size(int(M), int(K), ctypes.byref(b)), "lx_nvfp4_gemv_ws_size")
+    _check(_abi.load().lx_nvfp4_gemv_ws_size(int(M), int(N), int(K), ctypes.byref(b)), "lx_nvfp4_gemv_ws_size")
     return b.value
 
 
@@ -582,11 +582,13 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
     else:
         raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
     if ws is None:
-        ws = x.new_empty(lx_nvfp4_gemv_ws_size(M, K), dtype=torch.uint8)
+        size = lx_nvfp4_gemv_ws_size(M, N, K)
+        if size:
+            ws = x.new_empty(size, dtype=torch.uint8)
     status = _abi.load().lx_nvfp4_gemv(
         x.data_ptr(), M, strides[0] if M > 1 else max(strides[0], K), codes.data_ptr(), sf.data_ptr(), gw.data_ptr(),
-        None if bias is None else bias.data_ptr(), N, K, out.data_ptr(), ldy, ws.data_ptr(),
-        ws.numel() * ws.element_size(), _raw_stream(dev))
+        None if bias is None else bias.data_ptr(), N, K, out.data_ptr(), ldy,
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(dev))
     if status:
         _check(status, "lx_nvfp4_gemv")
     return out

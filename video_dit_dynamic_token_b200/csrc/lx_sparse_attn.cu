@@ -452,7 +452,7 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   lx_status st = check_packed(Q, K, V, O);
   if (st != LX_OK) return st;
   if (!pack || !pack->cu_q || !pack->cu_k || pack->n < 1) return LX_ERR_INVALID;
-  if (pack->n > (int64_t)1 << 30) return LX_ERR_UNSUPPORTED;
+  if (pack->n > (int64_t)1 << 20) return LX_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || !std::isfinite(scale)) return LX_ERR_INVALID;
   if ((reinterpret_cast<uintptr_t>(pack->cu_q) | reinterpret_cast<uintptr_t>(pack->cu_k) |
        reinterpret_cast<uintptr_t>(pack->len_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
@@ -533,23 +533,31 @@ int gemv_split(int64_t tiles, int64_t stages) {
 // Workspace: the digit rows [M P][K / 2], then the rows' exponents.
 inline int gemv_digits(int64_t M) { return M <= 8 ? 16 : 8; }
 inline size_t gemv_ref_offset(int64_t M, int64_t K) { return align256((size_t)(gemv_digits(M) * M) * (size_t)(K / 2)); }
-inline size_t gemv_ws_bytes(int64_t M, int64_t K) { return gemv_ref_offset(M, K) + 256; }
+inline bool gemv_own_digits(int64_t M, int64_t N, int64_t K) {
+  return M <= 8 && M * K <= lx::kGvOwnDigits && N * K <= lx::kGvOwnWeights;
+}
+inline size_t gemv_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  return gemv_own_digits(M, N, K) ? 0 : gemv_ref_offset(M, K) + 256;
+}
 
-template <int P>
+// OWN: the product kernel writes the digits (no workspace); else a pass before it.
+template <int P, bool OWN>
 lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
-  uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
-  int* ref = reinterpret_cast<int*>(ws + gemv_ref_offset(a.M, a.K));
-  a.ref = ref;
   const int64_t tiles = (a.N + lx::kGvTile - 1) / lx::kGvTile, stages = ((int64_t)a.K + 255) / 256;
   const int split = gemv_split(tiles, stages);
   a.per = (int)((stages + split - 1) / split);
+  uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
+  int* ref = OWN ? nullptr : reinterpret_cast<int*>(ws + gemv_ref_offset(a.M, a.K));
+  a.ref = ref;
+  a.stages = OWN ? lx::GemvOwnSmem::stages(a.M, a.per) : lx::GemvSmem<P>::stages(a.M);
   CUtensorMap tw, tx;
-  if (!make_map_codes(&tw, a.wc, a.N, a.K, lx::kGvTile) || !make_map_codes(&tx, codes, (int64_t)P * a.M, a.K, P * a.M))
+  if (!make_map_codes(&tw, a.wc, a.N, a.K, lx::kGvTile)) return LX_ERR_CUDA;
+  if (OWN) tx = tw;   // not read
+  if (!OWN && !make_map_codes(&tx, codes, (int64_t)P * a.M, a.K, P * a.M)) return LX_ERR_CUDA;
+  const int smem = (int)(OWN ? lx::GemvOwnSmem::bytes(a.M, a.per) : lx::GemvSmem<P>::bytes(a.M));
+  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<P, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return LX_ERR_CUDA;
-  const int smem = (int)lx::GemvSmem<P>::bytes(a.M);
-  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return LX_ERR_CUDA;
-  // both kernels start while the work ahead of them ends (they wait for it themselves)
+  // the kernels start while the work ahead of them ends (they wait for it themselves)
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -558,18 +566,20 @@ lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.M, (unsigned)(((int64_t)a.K + lx::kGvSlice - 1) / lx::kGvSlice));
-  cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_digits_kernel<P>, a.x, a.ldx, a.K, codes, ref) != cudaSuccess)
-    return LX_ERR_CUDA;
+  if (!OWN) {
+    cfg.gridDim = dim3((unsigned)a.M, (unsigned)(((int64_t)a.K + lx::kGvSlice - 1) / lx::kGvSlice));
+    cfg.blockDim = dim3(128);
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_digits_kernel<P>, a.x, a.ldx, a.K, codes, ref) != cudaSuccess)
+      return LX_ERR_CUDA;
+  }
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(lx::kGvThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<P>, tw, tx, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<P, OWN>, tw, tx, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
 }
 }  // namespace
 
@@ -1211,10 +1221,10 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
   return launch_status();
 }
 
-lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t K, size_t* bytes) {
-  if (!bytes || M < 1 || K < 64 || K % 64 != 0) return LX_ERR_INVALID;
-  if (M > lx::kGvMaxRows || K > ((int64_t)1 << 24)) return LX_ERR_UNSUPPORTED;
-  *bytes = gemv_ws_bytes(M, K);
+lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes || M < 1 || N < 1 || K < 64 || K % 64 != 0) return LX_ERR_INVALID;
+  if (M > lx::kGvMaxRows || N > ((int64_t)1 << 30) || K > ((int64_t)1 << 24)) return LX_ERR_UNSUPPORTED;
+  *bytes = gemv_ws_bytes(M, N, K);
   return LX_OK;
 }
 
@@ -1223,15 +1233,14 @@ lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc
                         cudaStream_t stream) {
   if (!x || !wc || !wsf || !gw || !y) return LX_ERR_INVALID;
   size_t need = 0;
-  lx_status st = lx_nvfp4_gemv_ws_size(M, K, &need);
+  lx_status st = lx_nvfp4_gemv_ws_size(M, N, K, &need);
   if (st != LX_OK) return st;
-  if (N < 1 || ldx < K || ldy < N) return LX_ERR_INVALID;
-  if (N > ((int64_t)1 << 30)) return LX_ERR_UNSUPPORTED;
+  if (ldx < K || ldy < N) return LX_ERR_INVALID;
   if (!al16(x) || ldx % 8 != 0 || !al16(wc) || !al16(wsf) || (reinterpret_cast<uintptr_t>(y) & 1u) ||
       ((reinterpret_cast<uintptr_t>(gw) | reinterpret_cast<uintptr_t>(bias)) & 3u))
     return LX_ERR_ALIGN;
-  if (!ws || ws_bytes < need) return LX_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
+  if (need && (!ws || ws_bytes < need)) return LX_ERR_WORKSPACE;
+  if (need && (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
   lx::GemvArgs a{};
   a.x = reinterpret_cast<const __nv_bfloat16*>(x);
   a.wc = wc;
@@ -1246,7 +1255,8 @@ lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc
   a.K = (int)K;
   a.limit_ns = kWaitLimitNs;
   char* base = reinterpret_cast<char*>(ws);
-  return gemv_digits(M) == 16 ? launch_gemv<16>(a, base, stream) : launch_gemv<8>(a, base, stream);
+  if (gemv_own_digits(M, N, K)) return launch_gemv<16, true>(a, nullptr, stream);
+  return gemv_digits(M) == 16 ? launch_gemv<16, false>(a, base, stream) : launch_gemv<8, false>(a, base, stream);
 }
 
 }  // extern "C"

@@ -58,6 +58,32 @@ struct GemvSmem {
   }
 };
 constexpr int kGvMaxStages = 5;
+// Up to this many elements of x, and up to this many weights, the product kernel writes the
+// digits itself, each CTA those of its range of K (8 bytes of shared memory an element): one
+// launch and no workspace, 4 us less of the host's time, which such calls wait for (two rows x
+// 5120 x 5120: 8.7 us on the device instead of 8.4).  Beyond, and for more than 8 rows, they
+// come from a pass of their own, as every CTA would read all of x and write its part again (two
+// rows x 30720 x 5120: 24.3 us, with the pass 21.6).
+constexpr int kGvOwnDigits = 10240;
+constexpr long long kGvOwnWeights = 1 << 25;
+constexpr uint32_t kGvSmemLimit = 227 * 1024 - 2048;
+struct GemvOwnSmem {
+  static constexpr uint32_t stage = kGvBBytes + kGvSfBytes;
+  __host__ __device__ static constexpr uint32_t x_bytes(int M, int per) { return 2048u * (uint32_t)(M * per); }
+  __host__ __device__ static constexpr uint32_t slack(int M) { return 128 * 128 - 2048u * (uint32_t)M; }
+  __host__ __device__ static constexpr int stages(int M, int per) {
+    const int fit = (int)((kGvSmemLimit - 1024 - x_bytes(M, per) - slack(M)) / stage);
+    return fit < kGvMaxStages ? fit : kGvMaxStages;
+  }
+  __host__ __device__ static constexpr uint32_t bytes(int M, int per) {
+    return 1024 + (uint32_t)stages(M, per) * stage + x_bytes(M, per) + slack(M);
+  }
+};
+static_assert(GemvOwnSmem::stages(1, kGvOwnDigits / 256) >= 3 &&
+                  3 * GemvOwnSmem::stage + GemvOwnSmem::x_bytes(1, kGvOwnDigits / 256) >= (128 + kGvMaxRows) * 1024 &&
+                  4 * GemvOwnSmem::stage >= (128 + kGvMaxRows) * 1024 &&
+                  GemvOwnSmem::stages(1, kGvOwnDigits / 512) >= 4,
+              "room for the stages and the sums");
 static_assert(GemvSmem<16>::bytes(1) <= 227 * 1024 - 2048 && GemvSmem<16>::bytes(2) <= 227 * 1024 - 2048 &&
                   GemvSmem<16>::bytes(8) <= 227 * 1024 - 2048 && GemvSmem<8>::bytes(16) <= 227 * 1024 - 2048,
               "shared memory per CTA");
@@ -77,6 +103,7 @@ struct GemvArgs {
   __nv_bfloat16* y;
   long long ldx, ldy, N;
   int M, K, per;        // per: 256-element stages of a CTA
+  int stages;           // ring slots
   unsigned long long limit_ns;
 };
 
@@ -139,6 +166,29 @@ __device__ __forceinline__ uint4 finite_only(uint4 v) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Largest finite magnitude (bits of a bf16) of pieces first, first + step, ... of a row, and bits that
+// are set where an element is not finite; over the warp.
+__device__ __forceinline__ void gemv_row_max(const uint4* row, int first, int pieces, int step, uint32_t& top,
+                                             uint32_t& bad) {
+  for (int v = first; v < pieces; v += 8 * step) {   // eight loads on their way together, also the last
+    uint4 t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v + i * step < pieces ? row[v + i * step] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (v - (int)(threadIdx.x & 31) + i * step >= pieces) break;   // (a warp together)
+      const uint4 f = finite_only(t[i]);
+      bad |= (f.x ^ t[i].x) | (f.y ^ t[i].y) | (f.z ^ t[i].z) | (f.w ^ t[i].w);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(f.x & 0x7FFF7FFFu, f.y & 0x7FFF7FFFu),
+                                   __vmaxu2(f.z & 0x7FFF7FFFu, f.w & 0x7FFF7FFFu)));
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+  bad = __reduce_or_sync(0xffffffffu, bad);
+}
+
+__device__ __forceinline__ int gemv_ref(uint32_t top, uint32_t bad) { return max(1, (int)(top >> 7)) | (bad ? kGvBadRow : 0); }
+
 // grid (M, ceil(K / kGvSlice)), 128 threads of 8 elements.  Every CTA reads the whole
 // row (it is short) for its largest element.  codes: [M P][K / 2], row m P + d holds
 // digit d of x's row m.
@@ -153,16 +203,8 @@ __global__ void __launch_bounds__(128) nvfp4_gemv_digits_kernel(const __nv_bfloa
   const int k = blockIdx.y * kGvSlice + threadIdx.x * 8;
   const uint4 mine = k < K ? row[k / 8] : make_uint4(0, 0, 0, 0);
   uint32_t top = 0, bad = 0;
-#pragma unroll 8
-  for (int v = threadIdx.x; v < K / 8; v += 128) {
-    const uint4 t = row[v], f = finite_only(t);
-    bad |= (f.x ^ t.x) | (f.y ^ t.y) | (f.z ^ t.z) | (f.w ^ t.w);
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(f.x & 0x7FFF7FFFu, f.y & 0x7FFF7FFFu),
-                                 __vmaxu2(f.z & 0x7FFF7FFFu, f.w & 0x7FFF7FFFu)));
-  }
+  gemv_row_max(row, threadIdx.x, K / 8, 128, top, bad);
   __shared__ uint32_t s_top[4], s_bad[4];
-  top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-  bad = __reduce_or_sync(0xffffffffu, bad);
   if ((threadIdx.x & 31) == 0) {
     s_top[threadIdx.x >> 5] = top;
     s_bad[threadIdx.x >> 5] = bad;
@@ -170,8 +212,8 @@ __global__ void __launch_bounds__(128) nvfp4_gemv_digits_kernel(const __nv_bfloa
   __syncthreads();
   top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
   bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
-  const int biased = max(1, (int)(top >> 7)), e = 21 + 127 - biased;    // 2^e, in two factors
-  if (blockIdx.y == 0 && threadIdx.x == 0) ref[m] = biased | (bad ? kGvBadRow : 0);
+  const int info = gemv_ref(top, bad), e = 21 + 127 - (info & 0xFFFF);  // 2^e, in two factors
+  if (blockIdx.y == 0 && threadIdx.x == 0) ref[m] = info;
   if (k >= K) return;
   uint32_t word[P];
   gemv_digits8<P>(bad ? finite_only(mine) : mine, pow2f(e >> 1), pow2f(e - (e >> 1)), word);
@@ -202,11 +244,11 @@ __device__ __forceinline__ void cluster_sync() {
 //           sums.  One set takes 1,000 clocks a stage, whose MMAs take 420.  tcgen05.cp
 //           does the same in the tensor pipe, where each copy of 512 bytes took 70
 //           clocks between MMAs of 105.
-// All ten warps then turn digit sums into outputs.  The digits' own scales are 1.  (Digits
-// made by warps of this kernel, stage by stage, were no faster for one row and cost
-// up to 40 us more for 16, every CTA reading its part of x twice.)  The CTAs of a cluster split K and add their sums over
+// All ten warps then turn digit sums into outputs.  The digits' own scales are 1.  OWN: warps
+// 2 .. 9 write the digits of the CTA's whole range first, under the first loads of the
+// weights.  (Stage by stage, for any number of rows, that cost up to 40 us more for 16.)  The CTAs of a cluster split K and add their sums over
 // distributed shared memory, in rank order.
-template <int P>
+template <int P, bool OWN>
 __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                    const __grid_constant__ CUtensorMap tmX,
                                                                    const GemvArgs a) {
@@ -226,8 +268,10 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int M = a.M, rows = M * P, stages = S::stages(M);
-  const uint32_t stage_bytes = S::stage(M);
+  const int M = a.M, rows = M * P, stages = a.stages;
+  const uint32_t stage_bytes = OWN ? GemvOwnSmem::stage : S::stage(M);
+  uint8_t* own = sm + stages * stage_bytes;                // OWN: digits, 128-byte rows, M P a stage
+  __shared__ uint32_t s_top[8], s_bad[8];                  // OWN: of a row of x
   const int KS = a.K / 64, nkb = (KS + 3) / 4;
   const int tile = blockIdx.x / ranks;
   const int kb0 = rank * a.per, n = min(a.per, nkb - kb0);   // stages of this CTA (at least one)
@@ -235,7 +279,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmX);
+    if constexpr (!OWN) prefetch_tensormap(&tmX);
     for (int s = 0; s < stages; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], 1);
@@ -245,6 +289,8 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
     mbar_init(&bar_drain, 1);
     abort_flag = 0;
     never_abort = 0;
+    if constexpr (OWN)
+      for (int m = 0; m < 8; ++m) s_top[m] = s_bad[m] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -258,13 +304,15 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
   int info = 0;                                              // of row `lane` of x
 
   if (warp == 0) {
+    // OWN: x first, which would otherwise wait in the memory system behind the weights
+    if constexpr (OWN) asm volatile("bar.sync 2, 288;" ::: "memory");
     if (lane == 0) {
       // ================= loads =================
       auto load_w = [&](int i) {
         const int s = i % stages, kb = kb0 + i;
         uint8_t* st = sm + s * stage_bytes;
         const uint32_t sfb = (uint32_t)min(4, KS - 4 * kb) * 512u;     // k-steps of 64 in the stage
-        mbar_arrive_expect_tx(&bar_full[s], kGvBBytes + S::x_bytes(M) + (has1 ? 2u : 1u) * sfb);
+        mbar_arrive_expect_tx(&bar_full[s], kGvBBytes + (OWN ? 0u : S::x_bytes(M)) + (has1 ? 2u : 1u) * sfb);
         tma_load_2d(st, &tmW, &bar_full[s], kb * 128, tile * 256);
         bulk_load(st + kGvBBytes, a.wsf + ((long long)(2 * tile) * KS + kb * 4) * 512, sfb, &bar_full[s]);
         if (has1)
@@ -275,16 +323,20 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
         tma_load_2d(sm + s * stage_bytes + kGvBBytes + kGvSfBytes, &tmX, &bar_full[s], (kb0 + i) * 128, 0);
       };
       const int first = min(n, stages);
+      // OWN: the work ahead may have written the weights; else the digit pass has waited for it
+      if constexpr (OWN) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int i = 0; i < first; ++i) load_w(i);
-      asm volatile("griddepcontrol.wait;" ::: "memory");               // the digits are complete
-      for (int i = 0; i < first; ++i) load_x(i);
+      if constexpr (!OWN) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");             // the digits are complete
+        for (int i = 0; i < first; ++i) load_x(i);
+      }
       bool ok = true;
       int i = first;
       for (; i < n; ++i) {
         ok = mbar_wait(&bar_empty[i % stages], (uint32_t)((i / stages) - 1) & 1u, &abort_flag, a.limit_ns);
         if (!ok) break;
         load_w(i);
-        load_x(i);
+        if constexpr (!OWN) load_x(i);
       }
       if (!ok) {
         abort_flag = 1;
@@ -302,7 +354,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
       // (the high word is common), slot and phase kept as they go (1,000 clocks a stage without
       // that, 850 with it; the MMAs take 450)
       const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, SW_128B);
-      const uint32_t hi = (uint32_t)(d0 >> 32);
+      const uint32_t hi = (uint32_t)(d0 >> 32), own_lo = (uint32_t)smem_desc(smem_u32(own), 16, 1024, SW_128B);
       const int last = KS - 4 * (kb0 + n - 1);       // k-steps of the last stage, if fewer than 4
       bool ok = true;
       uint32_t ph = 0;
@@ -311,7 +363,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
         ok = mbar_wait(&bar_full[s], ph, &abort_flag, a.limit_ns) && mbar_wait(&bar_sf[s], ph, &abort_flag, a.limit_ns);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t wlo = (uint32_t)d0 + s * (stage_bytes >> 4), xlo = wlo + ((kGvBBytes + kGvSfBytes) >> 4);
+        const uint32_t wlo = (uint32_t)d0 + s * (stage_bytes >> 4), xlo = OWN ? own_lo + i * (M * P * 128 >> 4) : wlo + ((kGvBBytes + kGvSfBytes) >> 4);
         const uint32_t tsf = tb + 288u + 32u * s;
         const int steps = i + 1 < n ? 4 : last;
 #pragma unroll
@@ -336,7 +388,39 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
     const int quarter = warp & 3, set = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     asm volatile("griddepcontrol.wait;" ::: "memory");                 // the digits and exponents are complete
-    info = a.ref[min(lane, M - 1)];
+    if constexpr (OWN) {
+      // the largest elements: 8 / M warps a row
+      const uint32_t w = warp - 2, per_row = 8u / (uint32_t)M;
+      if (w < per_row * M) {
+        const int m = w % (uint32_t)M;
+        uint32_t top = 0, bad = 0;
+        gemv_row_max(reinterpret_cast<const uint4*>(a.x + m * a.ldx), (int)(w / (uint32_t)M) * 32 + lane, a.K / 8,
+                     (int)per_row * 32, top, bad);
+        if (lane == 0) {
+          atomicMax(&s_top[m], top);
+          atomicOr(&s_bad[m], bad);
+        }
+      }
+      asm volatile("bar.arrive 2, 288;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      info = gemv_ref(s_top[min(lane, M - 1)], s_bad[min(lane, M - 1)]);
+      // digits of this CTA's range, a row of 256 elements by a warp
+      for (int q = (int)w; q < n * M; q += 8) {
+        const int i = q / M, m = q - i * M, k = (kb0 + i) * 256 + lane * 8;
+        const int f = __shfl_sync(0xffffffffu, info, m), e = 21 + 127 - (f & 0xFFFF);
+        const uint4 v = k < a.K ? *reinterpret_cast<const uint4*>(a.x + m * a.ldx + k) : make_uint4(0, 0, 0, 0);
+        uint32_t word[P];
+        gemv_digits8<P>(f & kGvBadRow ? finite_only(v) : v, pow2f(e >> 1), pow2f(e - (e >> 1)), word);
+        uint8_t* dst = own + (i * M + m) * (P * 128) + (lane & 3) * 4;
+#pragma unroll
+        for (int d = 0; d < P; ++d)   // the 16-byte pieces in the MMA's 128-byte swizzle
+          *reinterpret_cast<uint32_t*>(dst + d * 128 + (((lane >> 2) ^ (d & 7)) << 4)) = word[d];
+      }
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    } else {
+      info = a.ref[min(lane, M - 1)];
+    }
     if (set == 0) {
       uint32_t one[16];
 #pragma unroll
@@ -453,6 +537,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
     }
   }
   // every CTA of the cluster adds a share of the outputs, four at a time, in rank order
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the warps that have not waited yet
   cluster_sync();
   const float gw = *a.gw;
   const uint32_t base = smem_u32(part);

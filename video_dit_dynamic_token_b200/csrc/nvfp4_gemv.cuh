@@ -6,8 +6,8 @@
 // timestep, a guided pair, single new tokens).  The weights are read once: N K / 2
 // bytes of codes and N K / 16 of scales, which is what bounds large ones (30720 x 5120, cold:
 // one row 21.5 us = 4.1 TB/s, 120 of the 148 SMs having a tile; 8 and 16 rows 23.3).
-// Small ones are bound by the start of two kernels and the joining of sums (5120 x 5120, two
-// rows: 8.5 us; 256 x 512, one row: 5.7).
+// Small ones are bound by the start, the digits and the joining of sums (5120 x 5120, two
+// rows: 8.6 us; 256 x 512, one row: 5.9).
 //
 // Decoding 4-bit weights costs more issue slots than an SM has at the rate they
 // arrive (42 weights per clock; mma.sync on weights decoded to fp16 took 38 to 55 us
@@ -61,7 +61,7 @@ constexpr int kGvMaxStages = 5;
 // Up to this many elements of x, and up to this many weights, the product kernel writes the
 // digits itself, each CTA those of its range of K (8 bytes of shared memory an element): one
 // launch and no workspace, 4 us less of the host's time, which such calls wait for (two rows x
-// 5120 x 5120: 8.7 us on the device instead of 8.4).  Beyond, and for more than 8 rows, they
+// 5120 x 5120: 8.6 us on the device instead of 8.4).  Beyond, and for more than 8 rows, they
 // come from a pass of their own, as every CTA would read all of x and write its part again (two
 // rows x 30720 x 5120: 24.3 us, with the pass 21.6).
 constexpr int kGvOwnDigits = 10240;

@@ -318,9 +318,9 @@ typedef struct lx_pack {
   int64_t n;            /* sequences, 1 .. 2^20 */
 } lx_pack;
 
-/* Workspace of lx_attn_packed: 0 for prompts that fill the GPU without splitting
- * their keys and for at most 256 key rows; else at most 64 MB, or two splits' worth
- * for many rows. */
+/* Workspace of lx_attn_packed: 0 for prompts that give every SM two items or have at most
+ * 2048 key rows, and for at most 256 key rows; else at most 64 MB, or two splits' worth for
+ * many rows. */
 lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, size_t* bytes);
 
 /* Q, O [1, Hq, Tq, D]; K, V [1, Hkv, Tk, D], Hq a multiple of Hkv and at most 128

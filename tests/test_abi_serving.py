@@ -53,8 +53,9 @@ def test_packed_refusals(lib):
     for bad in (0.0, -1.0, float("inf"), float("nan")):
         assert _packed(lib, scale=bad) == INV
     assert _packed(lib, lse=0x5002) == ALI
-    assert _packed(lib, ws=None) == WSP
-    assert _packed(lib, ws=0x100010) == ALI
+    long = _view(H=2, L=3000)                                     # enough keys to split
+    assert _packed(lib, k=long, ws=None) == WSP
+    assert _packed(lib, k=long, ws=0x100010) == ALI
     r = ctypes.byref
     q, k, pk = _view(), _view(H=2), _pack()
     assert lib.lx_attn_packed(None, r(k), r(k), r(pk), 1, 0.1, r(q), None, 0x100000, 1 << 40, S) == INV

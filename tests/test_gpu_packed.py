@@ -146,7 +146,7 @@ def test_prompts_that_fill_the_gpu(lx, hq, hkv, D):
 
 
 def test_alone_and_in_a_large_pack(lx):
-    """The same sequences by themselves (keys split over the SMs) and in a pack that needs no split."""
+    """The same sequences by themselves and in a pack."""
     D, hq, hkv = 128, 40, 40
     lq = [400, 900, 130] * 4
     Q, K, V, out, lse = _run(lx, lq, lq, hq, hkv, D, True, seed=11, ref=False)
@@ -156,7 +156,6 @@ def test_alone_and_in_a_large_pack(lx):
         a, b = cu[i], cu[i + 1]
         l1 = torch.empty((hq, b - a), device=DEV)
         o1 = lx.lx_attn_packed(Q[:, :, a:b], K[:, :, a:b], V[:, :, a:b], _i32([0, b - a]), _i32([0, b - a]), lse=l1)
-        assert (lx.lx_attn_packed_ws_size(Q[:, :, a:b], K[:, :, a:b], 1) > 0) == (b - a > 256)
         assert lx.lx_last_device_status() == 0
         assert (o1 - out[:, :, a:b]).abs().max() <= 0.02
         assert (l1 - lse[:, a:b]).abs().max() <= 1e-4
@@ -359,3 +358,25 @@ def test_rows_of_the_output_at_16_and_32_bytes(lx, pad):
         rest = torch.cat((room[..., :first], room[..., first + 64:]), -1)
         assert torch.all(rest == 7.0)
         room.fill_(7.0)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,D,lq,lk", [(1, 1, 64, [2700], [2700]), (2, 2, 128, [2500], [2500]), (8, 2, 64, [700, 3, 40], [3100, 300, 40]),
+                                            (6, 2, 128, [300], [4000])])
+def test_few_long_prompts_are_split(lx, hq, hkv, D, lq, lk, causal):
+    """Too few row tiles for the SMs: the keys of full row tiles are split and joined."""
+    Q, K, V, out, lse = _run(lx, lq, lk, hq, hkv, D, causal, seed=sum(lk), spare=2, ref=False)
+    assert lx.lx_attn_packed_ws_size(Q, K, len(lq)) > 0
+    cq, ck = _cu(lq), _cu(lk)
+    rows = np.zeros((hq, cq[-1] + 2), bool)
+    for a, b in zip(cq, cq[1:]):   # every 37th row and the last of each sequence
+        rows[:, a:b:37] = rows[:, b - 1] = True
+    keep = np.flatnonzero(rows[0])
+    for h in (0, hq - 1):
+        g = h // (hq // hkv)
+        for i in range(len(lq)):
+            for t in keep[(keep >= cq[i]) & (keep < cq[i + 1])]:
+                n = lk[i] - lq[i] + (t - cq[i]) + 1 if causal else lk[i]
+                r = oracle.packed_attn_ref(_np(Q)[h:h + 1, t:t + 1], _np(K)[g:g + 1, ck[i]:ck[i] + n],
+                                           _np(V)[g:g + 1, ck[i]:ck[i] + n], [0, 1], [0, n], False, D ** -0.5)
+                _check(out[:, h:h + 1, t:t + 1], lse[h:h + 1, t:t + 1], r, D)

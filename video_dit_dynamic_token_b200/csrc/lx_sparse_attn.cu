@@ -368,11 +368,13 @@ bool make_map_grouped(CUtensorMap* m, const lx_bhld* t, int64_t Hkv, int tokens)
 
 inline int pack_tokens(int64_t G) { return (int)(128 / G); }
 
-// Prompts that give every SM several items, more than a row tile of each sequence on
-// average, gain nothing from splitting keys: such calls need no workspace.
-bool pack_fills(int64_t Tq, int64_t n, int64_t G, int64_t Hkv) {
-  const int64_t TQ = pack_tokens(G);
-  return Hkv * (Tq / (2 * TQ)) >= 3 * lx::kPkSMs && Tq > n * TQ;
+// Prompts (more than a row tile of each sequence on average) that give every SM two items, or
+// whose keys are too few to split, gain nothing from it (the estimate in pack_prepare): such calls
+// need no workspace.  24 prompts of 17 to 2,000 tokens take 170 us whole, 255 split; 1,100 tokens
+// over 77 to 512 keys 15 and 27.
+bool pack_wide(int64_t Tq, int64_t n, int64_t G) { return Tq > n * pack_tokens(G); }
+bool pack_fills(int64_t Tq, int64_t n, int64_t G, int64_t Hkv, int64_t Tk) {
+  return pack_wide(Tq, n, G) && (Hkv * (Tq / (2 * pack_tokens(G))) >= 2 * lx::kPkSMs || Tk <= 16 * lx::kPkKeys);
 }
 
 // Room for partial rows: as many splits as 64 MB hold, 2 to 128 (behind a prefix
@@ -384,7 +386,8 @@ struct PackWs {
 };
 PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D, int64_t Tk, bool prefix) {
   PackWs w{};
-  // no sequence is longer than two tiles: joining would cost more than it saves
+  // no sequence is longer than two tiles: joining would cost more than it saves (three prompts
+  // of 5 to 77 tokens 7.3 us, split 9.8)
   if (!prefix && Tk <= 2 * lx::kPkKeys) {
     w.splits = 1;
     return w;
@@ -460,7 +463,7 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   const int64_t G = Q->H / K->H;
   lx::PackParams p{};
   p.max_ns = 1;
-  if (Kp || !pack_fills(Q->L, pack->n, G, K->H)) {
+  if (Kp || !pack_fills(Q->L, pack->n, G, K->H, K->L)) {
     const PackWs w = pack_layout(Q->L, Q->H, Q->D, K->L, Kp != nullptr);
     if (w.total) {
       if (!ws || ws_bytes < w.total) return LX_ERR_WORKSPACE;
@@ -487,6 +490,7 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   p.Hkv = (int)K->H;
   p.TQ = pack_tokens(G);
   p.causal = causal != 0;
+  p.wide = !Kp && pack_wide(Q->L, pack->n, G);
   p.scale_log2 = (float)(1.4426950408889634 * (double)scale);
   p.pair = K->H % 2 == 0 ? 2 : 1;
   p.units = (int)(K->H / p.pair);
@@ -1017,7 +1021,7 @@ lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, 
   lx_status st;
   if ((st = check_packed(Q, K, K, Q)) != LX_OK) return st;
   if (!bytes || n < 1) return LX_ERR_INVALID;
-  *bytes = pack_fills(Q->L, n, Q->H / K->H, K->H) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, false).total;
+  *bytes = pack_fills(Q->L, n, Q->H / K->H, K->H, K->L) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, false).total;
   return LX_OK;
 }
 

@@ -73,7 +73,10 @@ namespace lx {
 constexpr int kPkKeys = 128;         // keys of a tile
 constexpr int kPkHalf = 64;          // keys of a product with V
 constexpr int kPkSplitKeys = 1;      // a split covers at least this many tiles (2: four tokens behind 200 keys 15.9, not 14.1 us)
-constexpr int kPkFine = 6;           // from this many tiles on, three splits for a CTA's share of the work
+// from this many tiles on, three splits for a CTA's share of the work (64 tokens behind 8,192 keys,
+// 16 over 1,000 to 4,000: 4 46.3 and 40.5 us, 6 44.4 and 46.8, 9 42.1 and 50.4; 75,600 shared keys:
+// two splits 195 us, three 172, four 186)
+constexpr int kPkFine = 6;
 constexpr int kPkSMs = 148;
 constexpr int kPkItems = 4;          // items published ahead of their last reader
 constexpr float kPkLazy = 8.0f;      // log2 growth of the row maximum that moves the reference
@@ -111,8 +114,9 @@ struct PackParams {
   float* lse;            // [Hq][Tq] or null
   float* part;           // [max_np + max_ns][Tq * Hq][D] unnormalised rows; null where nothing is split
   float2* ml;            // [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
-  int* chunk;            // tiles per split, for the combine kernel
+  int* chunk;            // tiles per split, whether nothing is split; for the combine kernel
   int max_np, max_ns;    // most splits of the prefix, of a sequence
+  int wide;              // more than a row tile of tokens a sequence on average, no prefix
   int pair, units;       // key/value heads of a narrow item (1 or 2), Hkv / pair
   int group;             // units worked on at a time
   unsigned long long limit_ns;
@@ -185,7 +189,7 @@ struct PackItem {
 // (p.pair key/value heads), and for up to 128 chunks of sequences the items before each.
 constexpr int kPkChunks = 128;
 struct PackTable {
-  unsigned long long work;
+  unsigned long long work, hidden;   // steps; those that the causal rule spares
   int longest;
   int c, np, pi;           // tiles per split, prefix splits, prefix items
   int total;               // items of a unit
@@ -210,26 +214,31 @@ __device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, in
 template <int THREADS>
 __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   const int tid = threadIdx.x;
-  if (tid == 0) tb.work = 0, tb.longest = 0, tb.np = 0, tb.pi = 0, tb.c = 0x7FFFFFFF;
+  if (tid == 0) tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0, tb.c = 0x7FFFFFFF;
   for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0;
   const PackSeq mine = tid < p.n ? pack_seq(p, tid) : PackSeq{0, 0, 0, 0};   // read once where it covers the table
   __syncthreads();
   if (p.part) {
     // the split length c follows from the work: a CTA's share of it, or a third of
     // that where it is long, so that uneven items still end together
-    unsigned long long w = 0;
+    unsigned long long w = 0, hid = 0;
     int l = 0;
     for (int i = tid; i < p.n; i += THREADS) {
       const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
       const int t = pack_tiles(s.lk);
       w += pack_steps(p, s.lq, t);
+      if (p.causal) hid += pack_steps(p, s.lq, min(t, pack_tiles(s.lq))) / 2;
       if (s.lq) l = max(l, t);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    for (int o = 16; o; o >>= 1) {
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+      hid += __shfl_xor_sync(0xffffffffu, hid, o);
+    }
     l = __reduce_max_sync(0xffffffffu, l);
     if ((tid & 31) == 0 && w) {
       atomicAdd(&tb.work, w);
+      atomicAdd(&tb.hidden, hid);
       atomicMax(&tb.longest, l);
     }
     __syncthreads();
@@ -240,12 +249,23 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
       if (c > kPkFine) c = max(kPkFine, pack_div(c, 3));
       c = max(max(c, kPkSplitKeys), pack_div(tb.longest, p.max_ns));
       if (p.Lp) c = max(c, pack_div(pt, p.max_np));
+      // Row tiles full of tokens pay for a split with their partial rows, about as much as 7
+      // tiles.  Times in tiles, fitted to single prompts of 2,000 to 16,128 tokens with 1 to 10
+      // heads (split, whole; 1.9 us a tile): 10 heads x 4,000 103, 66 us; 10 x 2,000 51, 36;
+      // 2 x 16,128 210, 223; 1 x 8,000 52, 118.
+      if (p.wide) {
+        const long long C = (long long)((work - tb.hidden * p.units + kPkSMs - 1) / kPkSMs), l = tb.longest;
+        if (max(l, C + l / 2) <= C + C / 2 + 7 * ((C + c - 1) / c) + 8) c = max(1, tb.longest);
+      }
       tb.c = c;
       if (p.Lp) {
         tb.np = pack_splits(p, rows, pt, c, p.max_np);
         tb.pi = pack_count(p, rows, tb.np);
       }
-      if (blockIdx.x == 0) *p.chunk = c;
+      if (blockIdx.x == 0) {
+        p.chunk[0] = c;
+        p.chunk[1] = p.wide && p.pair == 2 && c >= tb.longest;   // nothing to join
+      }
     }
     __syncthreads();
   }
@@ -1033,7 +1053,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
   const int Hq = p.Hkv * p.G, lane = threadIdx.x & 31;
   const long long R = (long long)p.Tq * Hq, row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");   // the partial rows are complete
-  if (row >= R) return;
+  if (row >= R || p.chunk[1]) return;
   const int tok = (int)(row / Hq), head = (int)(row % Hq);
   // the last sequence that starts at or before this token
   int lo = 0, hi = p.n;
@@ -1053,7 +1073,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
     if (tok < all.q0 || tok >= all.q0 + all.lq) return;
     rows = all.lq;
   }
-  const int c = *p.chunk;
+  const int c = p.chunk[0];
   const int np = p.Lp ? pack_splits(p, rows, pack_tiles(p.Lp), c, p.max_np) : 0;
   const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
   if (!p.Lp && ns == 1) return;   // its item finished the row

@@ -423,8 +423,9 @@ lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t
   const int64_t all = (p.Tq + rows - 1) / rows, prefix = p.Lp ? all : 0;
   const int64_t work = p.units * all * (p.Tk / lx::kPkKeys + p.n + (p.Lp + lx::kPkKeys - 1) / lx::kPkKeys);
   const int64_t splits = !p.part ? 0 : std::min({work, std::max<int64_t>(lx::kPkSMs, work / lx::kPkFine), (int64_t)3 * lx::kPkSMs});
-  const int64_t items = splits + (tiles + prefix) * p.units, blocks = ((int64_t)p.Tq * p.Hkv * p.G + 7) / 8;
-  if (items > 0x7FFFFFFE || blocks > 0x7FFFFFFF) return LX_ERR_UNSUPPORTED;
+  const int64_t items = splits + (tiles + prefix) * p.units;
+  const int64_t blocks = std::min<int64_t>(((int64_t)p.Tq * p.Hkv * p.G + 7) / 8, 3 * lx::kPkSMs);
+  if (items > 0x7FFFFFFE) return LX_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(lx::packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
     return LX_ERR_CUDA;

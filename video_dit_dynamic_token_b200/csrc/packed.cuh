@@ -262,10 +262,9 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
         tb.np = pack_splits(p, rows, pt, c, p.max_np);
         tb.pi = pack_count(p, rows, tb.np);
       }
-      if (blockIdx.x == 0) {
-        p.chunk[0] = c;
-        p.chunk[1] = p.wide && p.pair == 2 && c >= tb.longest;   // nothing to join
-      }
+      // by every CTA, all the same: which block numbers ever start is the launch control's affair
+      p.chunk[0] = c;
+      p.chunk[1] = p.wide && p.pair == 2 && c >= tb.longest;   // nothing to join
     }
     __syncthreads();
   }
@@ -1045,91 +1044,93 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   }
 }
 
-// Joins the splits of each row: a warp per row, lane = D / 32 channels, splits in
+// Joins the splits of each row: a warp per row (three CTAs per SM walk them), lane = D / 32 channels, splits in
 // ascending order (the result does not depend on which item finished first).
 template <int D>
 __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p) {
   constexpr int E = D / 32;
   const int Hq = p.Hkv * p.G, lane = threadIdx.x & 31;
-  const long long R = (long long)p.Tq * Hq, row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long R = (long long)p.Tq * Hq;
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");   // the partial rows are complete
-  if (row >= R || p.chunk[1]) return;
-  const int tok = (int)(row / Hq), head = (int)(row % Hq);
-  // the last sequence that starts at or before this token
-  int lo = 0, hi = p.n;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, at < hi && p.cu_q[at] <= tok);
-    const int k = le ? 31 - __clz(le) : 0;
-    const int nl = lo + k * step;
-    hi = min(hi, nl + step);
-    lo = nl;
-  }
-  const PackSeq s = pack_seq(p, lo);
-  if (tok < s.q0 || tok >= s.q0 + s.lq) return;
-  int rows = 0;
-  if (p.Lp) {  // a malformed table may leave rows without their prefix part
-    const PackSeq all = pack_all(p);
-    if (tok < all.q0 || tok >= all.q0 + all.lq) return;
-    rows = all.lq;
-  }
-  const int c = p.chunk[0];
-  const int np = p.Lp ? pack_splits(p, rows, pack_tiles(p.Lp), c, p.max_np) : 0;
-  const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
-  if (!p.Lp && ns == 1) return;   // its item finished the row
-  float m = -INFINITY, l = 0.f, o[E];
+  if (p.chunk[1]) return;
+  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < R; row += (long long)gridDim.x * 8) {
+    const int tok = (int)(row / Hq), head = (int)(row % Hq);
+    // the last sequence that starts at or before this token
+    int lo = 0, hi = p.n;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const unsigned le = __ballot_sync(0xffffffffu, at < hi && p.cu_q[at] <= tok);
+      const int k = le ? 31 - __clz(le) : 0;
+      const int nl = lo + k * step;
+      hi = min(hi, nl + step);
+      lo = nl;
+    }
+    const PackSeq s = pack_seq(p, lo);
+    if (tok < s.q0 || tok >= s.q0 + s.lq) continue;
+    int rows = 0;
+    if (p.Lp) {  // a malformed table may leave rows without their prefix part
+      const PackSeq all = pack_all(p);
+      if (tok < all.q0 || tok >= all.q0 + all.lq) continue;
+      rows = all.lq;
+    }
+    const int c = p.chunk[0];
+    const int np = p.Lp ? pack_splits(p, rows, pack_tiles(p.Lp), c, p.max_np) : 0;
+    const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
+    if (!p.Lp && ns == 1) continue;   // its item finished the row
+    float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  // 32 splits at a time, a weight in each lane; the rows of 8 are on their way together, with
-  // the maxima and sums (one after another: 10.8 us instead of 8.3 for 2,560 rows of 12 splits)
-  for (int b = 0; b < np + ns; b += 32) {
-    const int count = min(32, np + ns - b);
-    const long long base = (long long)b * R + row;
-    const float2 x = lane < count ? p.ml[base + lane * R] : make_float2(-INFINITY, 0.f);
-    float w = 0.f;
-    for (int i = 0; i < count; i += 8) {
-      float y[8][E];
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    // 32 splits at a time, a weight in each lane; the rows of 8 are on their way together, with
+    // the maxima and sums (one after another: 10.8 us instead of 8.3 for 2,560 rows of 12 splits)
+    for (int b = 0; b < np + ns; b += 32) {
+      const int count = min(32, np + ns - b);
+      const long long base = (long long)b * R + row;
+      const float2 x = lane < count ? p.ml[base + lane * R] : make_float2(-INFINITY, 0.f);
+      float w = 0.f;
+      for (int i = 0; i < count; i += 8) {
+        float y[8][E];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float* src = p.part + (base + (i + u) * R) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 z = i + u < count ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-          y[u][0] = z.x, y[u][1] = z.y, y[u][2] = z.z, y[u][3] = z.w;
-        } else {
-          const float2 z = i + u < count ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
-          y[u][0] = z.x, y[u][1] = z.y;
+        for (int u = 0; u < 8; ++u) {
+          const float* src = p.part + (base + (i + u) * R) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 z = i + u < count ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+            y[u][0] = z.x, y[u][1] = z.y, y[u][2] = z.z, y[u][3] = z.w;
+          } else {
+            const float2 z = i + u < count ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+            y[u][0] = z.x, y[u][1] = z.y;
+          }
+        }
+        if (i == 0) {
+          float top = fmaxf(m, x.x);
+#pragma unroll
+          for (int v = 16; v; v >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, v));
+          const float at = top == -INFINITY ? 0.f : top, a = ex2f(m - at);   // 0 from -inf
+          w = ex2f(x.x - at);
+          float sum = w * x.y;
+#pragma unroll
+          for (int v = 16; v; v >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, v);
+          l = fmaf(l, a, sum);
+          m = top;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] *= a;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w, (i + u) & 31);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(wu, y[u][e], o[e]);
         }
       }
-      if (i == 0) {
-        float top = fmaxf(m, x.x);
-#pragma unroll
-        for (int v = 16; v; v >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, v));
-        const float at = top == -INFINITY ? 0.f : top, a = ex2f(m - at);   // 0 from -inf
-        w = ex2f(x.x - at);
-        float sum = w * x.y;
-#pragma unroll
-        for (int v = 16; v; v >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, v);
-        l = fmaf(l, a, sum);
-        m = top;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= a;
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float wu = __shfl_sync(0xffffffffu, w, (i + u) & 31);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(wu, y[u][e], o[e]);
-      }
     }
-  }
-  const int seen = p.causal ? max(0, min(s.lk, tok - s.q0 + s.lk - s.lq + 1)) : s.lk;
-  const bool any = p.Lp > 0 || seen > 0;
-  __nv_bfloat16* dst = p.o + head * p.osH + tok * p.osL + lane * E;
+    const int seen = p.causal ? max(0, min(s.lk, tok - s.q0 + s.lk - s.lq + 1)) : s.lk;
+    const bool any = p.Lp > 0 || seen > 0;
+    __nv_bfloat16* dst = p.o + head * p.osH + tok * p.osL + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + e) =
-        any ? __floats2bfloat162_rn(o[e] / l, o[e + 1] / l) : __floats2bfloat162_rn(0.f, 0.f);
-  if (lane == 0 && p.lse) p.lse[(long long)head * p.Tq + tok] = any ? pack_lse(m, l) : -INFINITY;
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+          any ? __floats2bfloat162_rn(o[e] / l, o[e + 1] / l) : __floats2bfloat162_rn(0.f, 0.f);
+    if (lane == 0 && p.lse) p.lse[(long long)head * p.Tq + tok] = any ? pack_lse(m, l) : -INFINITY;
+  }
 }
 
 }  // namespace lx

@@ -214,7 +214,7 @@ __device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, in
 template <int THREADS>
 __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   const int tid = threadIdx.x;
-  if (tid == 0) tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0, tb.c = 0x7FFFFFFF;
+  if (tid == 0) tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0, tb.c = 1 << 29;   // one split
   for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0;
   const PackSeq mine = tid < p.n ? pack_seq(p, tid) : PackSeq{0, 0, 0, 0};   // read once where it covers the table
   __syncthreads();

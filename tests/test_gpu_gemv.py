@@ -237,3 +237,22 @@ def test_digits_in_the_product_kernel_and_before_it(lx, M, N, K):
     got = z[0].float().cpu().numpy()
     assert np.all(got[w > 0] == np.inf) and np.all(got[w < 0] == -np.inf) and np.all(np.isnan(got[w == 0]))
     assert torch.equal(z[1:], y[1:])
+
+
+@pytest.mark.parametrize("M", [1, 8, 16])
+def test_many_turns_of_the_ring(lx, M):
+    """Many stages a CTA, again and again beside copies that hold up the loads: no wait runs out, nothing changes."""
+    rng = np.random.default_rng(20 + M)
+    N, K = 2700, 30720
+    wq, wr = _weights(lx, rng, N, K)
+    x = _bf16(rng.standard_normal((M, K)))
+    first = _check(lx, x, wq, wr)
+    a = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    b, side = torch.empty_like(a), torch.cuda.Stream()
+    for _ in range(40):
+        with torch.cuda.stream(side):
+            b.copy_(a)
+        y = lx.lx_nvfp4_gemv(x, wq)
+        assert torch.equal(y, first)
+    torch.cuda.synchronize()
+    assert lx.lx_last_device_status() == 0

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
     if constexpr (!OWN) prefetch_tensormap(&tmX);
     for (int s = 0; s < stages; ++s) {
       mbar_init(&bar_full[s], 1);
-      mbar_init(&bar_empty[s], 1);
+      mbar_init(&bar_empty[s], 1 + 4);   // the MMA and the set of scale warps whose stage it is not
       mbar_init(&bar_sf[s], 4);
     }
     mbar_init(&bar_acc, 1);
@@ -435,7 +435,13 @@ __global__ void __launch_bounds__(kGvThreads, 1) nvfp4_gemv_kernel(const __grid_
       const int s = slot, steps = min(4, KS - 4 * (kb0 + i));
       ok = warp_wait(&bar_full[s], ph, &abort_flag, a.limit_ns);
       if (!ok) break;
-      if ((i & 1) != set) continue;   // the other set's; waited for all the same, as phases alternate
+      if ((i & 1) != set) {
+        // The other set's: this one only keeps up with the phases.  The slot may not be filled again
+        // before it has, as a phase's parity does not show a turn of the ring.  (A set holds back its
+        // own stages by bar_sf, which the MMA waits for.)
+        if (lane == 0) mbar_arrive(&bar_empty[s]);
+        continue;
+      }
       const uint4* sf = reinterpret_cast<const uint4*>(sm + s * stage_bytes + kGvBBytes) + lane;
       uint32_t v[32];
 #pragma unroll

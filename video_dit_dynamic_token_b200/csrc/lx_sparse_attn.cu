@@ -102,19 +102,32 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// Encodes a map.  That needs a current context, which a host thread without a CUDA call of its own does not
+// have yet: it gets its device's (cudaSetDevice binds it), and the map is tried again.
+template <int N>
+bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, const cuuint64_t (&dims)[N],
+                const cuuint64_t (&strides)[N - 1], const cuuint32_t (&box)[N], CUtensorMapSwizzle sw) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint32_t es[N];
+  for (int i = 0; i < N; ++i) es[i] = 1;
+  auto encode = [&]() {
+    return fn(m, dt, N, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
+
 // 4-D map over [B,H,L,D] (innermost first: D, L, H, B), strides in elements.
 bool make_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int esz, int64_t B, int64_t H, int64_t L,
               int64_t D, int64_t sB, int64_t sH, int64_t sL, int box_inner, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)(sL * esz), (cuuint64_t)(sH * esz), (cuuint64_t)(sB * esz)};
   const cuuint32_t box[4] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  const int inner_bytes = box_inner * esz;
-  const CUtensorMapSwizzle sw = inner_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  return fn(m, dt, 4, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map<4>(m, dt, ptr, dims, strides, box,
+                       box_inner * esz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -337,15 +350,10 @@ lx_status launch_ulysses(lx::UlyssesArgs a, int64_t D, cudaStream_t s) {
 // 2-D byte map over NVFP4 codes [rows][K/2] (innermost first), 128-byte swizzle,
 // box of 128 bytes x box_rows rows; rows past the end read as zero.
 bool make_map_codes(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
   const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map<2>(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -354,16 +362,11 @@ bool make_map_codes(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, in
 namespace {
 // Q as (channel, head in group, token, key/value head): one load brings TQ tokens x G heads
 bool make_map_grouped(CUtensorMap* m, const lx_bhld* t, int64_t Hkv, int tokens) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
   const int64_t G = t->H / Hkv;
   const cuuint64_t dims[4] = {(cuuint64_t)t->D, (cuuint64_t)G, (cuuint64_t)t->L, (cuuint64_t)Hkv};
   const cuuint64_t strides[3] = {(cuuint64_t)(t->sH * 2), (cuuint64_t)(t->sL * 2), (cuuint64_t)(t->sH * G * 2)};
   const cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)tokens, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map<4>(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t->data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 inline int pack_tokens(int64_t G) { return (int)(128 / G); }

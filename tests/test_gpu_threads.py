@@ -1,4 +1,5 @@
-"""Calls from host threads of the user's own."""
+"""Calls from host threads of the user's own, and a sound call after one that CUDA refused."""
+import ctypes
 import threading
 
 import pytest
@@ -16,6 +17,50 @@ def lx():
 
 def _rand(gen, *shape):
     return torch.randn(shape, generator=gen).to(torch.bfloat16).to(DEV)
+
+
+def test_a_refused_launch_leaves_no_error_behind(lx):
+    """A stream whose capture was broken refuses launches; the next call on another stream is sound and says so."""
+    lib = lx._abi.load()
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = _rand(gen, 1, 4, 9, 64), _rand(gen, 1, 2, 400, 64), _rand(gen, 1, 2, 400, 64)
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in (9, 400))
+    w = lx.lx_nvfp4_quantize(_rand(gen, 256, 512))
+    x, y = _rand(gen, 2, 512), torch.zeros((2, 256), dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros_like(q)
+    ws = torch.empty(lx.lx_attn_packed_ws_size(q, k, 1), dtype=torch.uint8, device=DEV)
+    means = [torch.zeros((1, 4, 1, 64), device=DEV) for _ in range(2)]
+    packed = lambda: lx.lx_attn_packed(q, k, v, cu_q, cu_k, out=out, ws=ws)
+    few = lambda: lx.lx_nvfp4_gemv(x, w, out=y)
+    few(), packed()
+    torch.cuda.synchronize()
+    want = out.clone(), y.clone()
+    broken, good = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    refused = 0
+    with torch.cuda.stream(broken):
+        graph.capture_begin(capture_error_mode="relaxed")
+        try:
+            with pytest.raises(RuntimeError):
+                broken.synchronize()      # not allowed in a capture: breaks it
+            for call in (packed, few):
+                with pytest.raises(lx.LxError):
+                    call()
+                refused += 1
+                with torch.cuda.stream(good):
+                    sq, sk = lx.bhld(q), lx.bhld(q)
+                    assert lib.lx_pool_means(sq, sk, means[0].data_ptr(), means[1].data_ptr(),
+                                             ctypes.c_void_p(good.cuda_stream)) == 0
+                    packed(), few()
+        finally:
+            try:
+                graph.capture_end()
+            except RuntimeError:
+                pass
+    assert refused == 2
+    torch.cuda.synchronize()
+    assert lx.lx_last_device_status() == 0
+    assert torch.equal(out, want[0]) and torch.equal(y, want[1])
 
 
 def test_first_call_of_a_thread(lx):

@@ -84,6 +84,12 @@ inline size_t score_ws_bytes(int64_t BH, int64_t nB) {
 inline lx_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? LX_OK : LX_ERR_CUDA;
 }
+// A failed CUDA call leaves its error with the host thread; it is taken out here, so that the
+// thread's next call does not report it as its own.
+inline lx_status cuda_failed() {
+  cudaGetLastError();
+  return LX_ERR_CUDA;
+}
 
 // ---------------------------------------------------------------- TMA maps
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -98,6 +104,8 @@ EncodeTiledFn encode_fn() {
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
+    else
+      cudaGetLastError();
   }
   return fn;
 }
@@ -166,7 +174,7 @@ lx_status launch_score_gemm(const float* mq, const float* mk, int64_t BH, int64_
   const size_t gsmem = 1024 + lx::kSgSmem;
   if (cudaFuncSetAttribute(lx::score_gemm_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gsmem) !=
       cudaSuccess)
-    return LX_ERR_CUDA;
+    return cuda_failed();
   dim3 ggrid((unsigned)((nB + lx::kSgM - 1) / lx::kSgM), (unsigned)((nB + lx::kSgN - 1) / lx::kSgN), (unsigned)BH);
   const int ldS = (int)score_ld(nB);
   lx::score_gemm_kernel<D><<<ggrid, 128, gsmem, s>>>(tq, tk, scores, (int)nB, ldS, kWaitLimitNs);
@@ -181,9 +189,8 @@ lx_status launch_select(const float* scores, int64_t BH, int64_t nB, int64_t k, 
   const size_t smem = sizeof(float) * ((size_t)lx::kScoreRows * ldS +
                                        lx::kScoreWarps * (lx::kBuckets + 2 * lx::kCandCap + ldS / 32));
   if (smem > 227 * 1024) return LX_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(lx::select_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return LX_ERR_CUDA;
+  if (cudaFuncSetAttribute(lx::select_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return cuda_failed();
   dim3 grid((unsigned)((nB + lx::kScoreRows - 1) / lx::kScoreRows), (unsigned)BH);
   lx::select_topk_kernel<<<grid, 32 * lx::kScoreWarps, smem, s>>>(scores, (int)nB, (int)k, idx, mask, ldS,
                                                                    kWaitLimitNs);
@@ -210,11 +217,11 @@ template <int D>
 lx_status launch_quant_v(const lx_bhld* V, uint8_t* vc, float* vs, uint32_t* amax, cudaStream_t s) {
   const int64_t BH = V->B * V->H, nB = n_blocks(V->L);
   const int nSpan = (int)((V->L + lx::kVSpan - 1) / lx::kVSpan);
-  if (cudaMemsetAsync(amax, 0, sizeof(uint32_t) * BH * D, s) != cudaSuccess) return LX_ERR_CUDA;
+  if (cudaMemsetAsync(amax, 0, sizeof(uint32_t) * BH * D, s) != cudaSuccess) return cuda_failed();
   lx::v_absmax_kernel<D><<<(unsigned)(BH * nSpan), 128, 0, s>>>(view(V), amax, (int)V->H, (int)V->L, nSpan);
-  if (cudaGetLastError() != cudaSuccess) return LX_ERR_CUDA;
+  if (launch_status() != LX_OK) return LX_ERR_CUDA;
   long long ctas = 0, per = 0;
-  if (!persistent_grid(BH * nB, &ctas, &per)) return LX_ERR_CUDA;
+  if (!persistent_grid(BH * nB, &ctas, &per)) return cuda_failed();
   lx::v_quant_kernel<D><<<(unsigned)ctas, 128, 0, s>>>(view(V), amax, vc, vs, (int)V->H, (int)V->L, (int)nB,
                                                        (long long)(BH * nB), per);
   return launch_status();
@@ -254,9 +261,8 @@ lx_status launch_attn_paired(const CUtensorMap& mq, const CUtensorMap& mk, const
   // the two kept lists follow the tiles
   const size_t smem = 1024 + C::OFF_IDX + 2 * sizeof(int32_t) * (size_t)plan->k;
   if (smem > 227 * 1024) return LX_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(lx::sparse_attn_paired_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return LX_ERR_CUDA;
+  if (cudaFuncSetAttribute(lx::sparse_attn_paired_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return cuda_failed();
   lx::sparse_attn_paired_kernel<D, true><<<attn_grid(plan), 192, smem, s>>>(mq, mk, mv,
                                                                            attn_params<D>(plan, O, qs, ks, vs));
   return launch_status();
@@ -270,9 +276,8 @@ lx_status launch_attn(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   // the two kept lists and their K scales follow the tiles
   const size_t smem = 1024 + C::OFF_IDX + 16 * (size_t)plan->k;
   if (smem > 227 * 1024) return LX_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(lx::sparse_attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return LX_ERR_CUDA;
+  if (cudaFuncSetAttribute(lx::sparse_attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return cuda_failed();
   lx::sparse_attn_kernel<D, I8><<<attn_grid(plan), C::THREADS, smem, s>>>(mq, mk, mv,
                                                                           attn_params<D>(plan, O, qs, ks, vs));
   return launch_status();
@@ -431,7 +436,7 @@ lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t
   if (items > 0x7FFFFFFE) return LX_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(lx::packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
-    return LX_ERR_CUDA;
+    return cuda_failed();
   // both kernels start while the work ahead of them ends (they wait for it themselves)
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -444,12 +449,12 @@ lx_status run_packed(const CUtensorMap* t, const lx::PackParams& p, cudaStream_t
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, lx::packed_attn_kernel<D>, t[0], t[1], t[2], t[3], t[4], p) != cudaSuccess)
-    return LX_ERR_CUDA;
-  if (!p.part) return launch_status();
+    return cuda_failed();
+  if (!p.part) return LX_OK;
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, lx::packed_combine_kernel<D>, p) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lx::packed_combine_kernel<D>, p) == cudaSuccess ? LX_OK : cuda_failed();
 }
 
 // Both entry points: Kp, Vp null without a prefix.
@@ -564,7 +569,7 @@ lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
   if (!OWN && !make_map_codes(&tx, codes, (int64_t)P * a.M, a.K, P * a.M)) return LX_ERR_CUDA;
   const int smem = (int)(OWN ? lx::GemvOwnSmem::bytes(a.M, a.per) : lx::GemvSmem<P>::bytes(a.M));
   if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<P, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return LX_ERR_CUDA;
+    return cuda_failed();
   // the kernels start while the work ahead of them ends (they wait for it themselves)
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -581,13 +586,13 @@ lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
     cfg.blockDim = dim3(128);
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_digits_kernel<P>, a.x, a.ldx, a.K, codes, ref) != cudaSuccess)
-      return LX_ERR_CUDA;
+      return cuda_failed();
   }
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(lx::kGvThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<P, OWN>, tw, tx, a) == cudaSuccess ? launch_status() : LX_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lx::nvfp4_gemv_kernel<P, OWN>, tw, tx, a) == cudaSuccess ? LX_OK : cuda_failed();
 }
 }  // namespace
 
@@ -786,7 +791,7 @@ lx_status lx_k_channel_mean(const lx_bhld* K, void* ws, size_t ws_bytes, float* 
     lx::k_mean_partial_kernel<128><<<(unsigned)(BH * nSpan), 128, 0, stream>>>(view(K), part, (int)K->H, (int)K->L, nSpan);
   else
     lx::k_mean_partial_kernel<64><<<(unsigned)(BH * nSpan), 128, 0, stream>>>(view(K), part, (int)K->H, (int)K->L, nSpan);
-  if (cudaGetLastError() != cudaSuccess) return LX_ERR_CUDA;
+  if (launch_status() != LX_OK) return LX_ERR_CUDA;
   const long long n = BH * K->D;
   lx::k_mean_final_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(part, km, BH, (int)K->D, nSpan, (int)K->L);
   return launch_status();
@@ -859,7 +864,7 @@ CtxGetCurrentFn ctx_get_current_fn() {
 // (device, context).
 lx_status noalloc_scratch(uint32_t** out) {
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return LX_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return cuda_failed();
   if (dev >= kMaxDevices) return LX_ERR_UNSUPPORTED;
   CtxGetCurrentFn get_ctx = ctx_get_current_fn();
   if (!get_ctx) return LX_ERR_CUDA;
@@ -870,7 +875,7 @@ lx_status noalloc_scratch(uint32_t** out) {
   if (!e.ptr || !ctx || e.ctx != ctx) {
     // the lookup also makes the runtime's context current when none is yet
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_noalloc_amax) != cudaSuccess || !p) return LX_ERR_CUDA;
+    if (cudaGetSymbolAddress(&p, g_noalloc_amax) != cudaSuccess || !p) return cuda_failed();
     if (get_ctx(&ctx) != CUDA_SUCCESS || !ctx) return LX_ERR_CUDA;
     e.ctx = ctx;
     e.ptr = static_cast<uint32_t*>(p);
@@ -1005,11 +1010,11 @@ lx_status lx_sparse_attn(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, d
 }
 
 lx_status lx_last_device_status(cudaStream_t stream) {
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return LX_ERR_CUDA;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return cuda_failed();
   int v = 0;
-  if (cudaMemcpyFromSymbol(&v, lx::g_device_status, sizeof(int)) != cudaSuccess) return LX_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(&v, lx::g_device_status, sizeof(int)) != cudaSuccess) return cuda_failed();
   const int zero = 0;
-  if (v != 0 && cudaMemcpyToSymbol(lx::g_device_status, &zero, sizeof(int)) != cudaSuccess) return LX_ERR_CUDA;
+  if (v != 0 && cudaMemcpyToSymbol(lx::g_device_status, &zero, sizeof(int)) != cudaSuccess) return cuda_failed();
   if (v == LX_ERR_TIMEOUT || v == LX_ERR_PLAN) return (lx_status)v;
   return v == 0 ? LX_OK : LX_ERR_CUDA;
 }
@@ -1176,10 +1181,10 @@ lx_status lx_nvfp4_quantize(const void* x, int64_t R, int64_t K, int64_t ldx, in
     return LX_ERR_ALIGN;
   const auto* xb = reinterpret_cast<const __nv_bfloat16*>(x);
   if (compute_gscale) {
-    if (cudaMemsetAsync(gscale, 0, sizeof(float), stream) != cudaSuccess) return LX_ERR_CUDA;
+    if (cudaMemsetAsync(gscale, 0, sizeof(float), stream) != cudaSuccess) return cuda_failed();
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return LX_ERR_CUDA;
+      return cuda_failed();
     const int64_t ctas = R < 8LL * sms ? R : 8LL * sms;
     lx::nvfp4_amax_kernel<<<(unsigned)ctas, 256, 0, stream>>>(xb, R, (int)K, ldx, reinterpret_cast<unsigned*>(gscale));
     lx::nvfp4_gscale_kernel<<<1, 1, 0, stream>>>(gscale);
@@ -1206,7 +1211,7 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
   if (!make_map_codes(&ta, xc, M, K, lx::kNvBM) || !make_map_codes(&tw, wc, N, K, lx::kNvBN)) return LX_ERR_CUDA;
   if (cudaFuncSetAttribute(lx::nvfp4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lx::kNvSmemBytes) !=
       cudaSuccess)
-    return LX_ERR_CUDA;
+    return cuda_failed();
   lx::NvGemmArgs a{};
   a.sfa = xsf;
   a.sfb = wsf;
@@ -1222,7 +1227,7 @@ lx_status lx_nvfp4_gemm(const uint8_t* xc, const uint8_t* xsf, const float* gx, 
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       sms < 1)
-    return LX_ERR_CUDA;
+    return cuda_failed();
   const int64_t tiles = mtiles * ntiles;  // persistent: one CTA per SM walks the tiles
   const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
   lx::nvfp4_gemm_kernel<<<grid, lx::kNvThreads, lx::kNvSmemBytes, stream>>>(ta, tw, a);

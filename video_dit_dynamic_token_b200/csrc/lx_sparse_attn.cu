@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -89,6 +90,23 @@ inline lx_status launch_status() {
 inline lx_status cuda_failed() {
   cudaGetLastError();
   return LX_ERR_CUDA;
+}
+
+// Lets a kernel have all the dynamic shared memory that a block can.  The limit belongs to the kernel, not to
+// a call: set to each call's own size, it could change between another host thread's setting and
+// its launch, which would then be refused.
+template <auto kKernel>
+lx_status allow_most_shared() {
+  static std::atomic<int> most{0};   // the same for every B200; host threads that race write the same
+  int bytes = most.load(std::memory_order_relaxed);
+  if (bytes == 0) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, kKernel) != cudaSuccess) return cuda_failed();
+    most.store(bytes = 227 * 1024 - (int)a.sharedSizeBytes, std::memory_order_relaxed);
+  }
+  return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
+             ? LX_OK
+             : cuda_failed();
 }
 
 // ---------------------------------------------------------------- TMA maps
@@ -189,8 +207,8 @@ lx_status launch_select(const float* scores, int64_t BH, int64_t nB, int64_t k, 
   const size_t smem = sizeof(float) * ((size_t)lx::kScoreRows * ldS +
                                        lx::kScoreWarps * (lx::kBuckets + 2 * lx::kCandCap + ldS / 32));
   if (smem > 227 * 1024) return LX_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(lx::select_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return cuda_failed();
+  const lx_status st = allow_most_shared<lx::select_topk_kernel>();
+  if (st != LX_OK) return st;
   dim3 grid((unsigned)((nB + lx::kScoreRows - 1) / lx::kScoreRows), (unsigned)BH);
   lx::select_topk_kernel<<<grid, 32 * lx::kScoreWarps, smem, s>>>(scores, (int)nB, (int)k, idx, mask, ldS,
                                                                    kWaitLimitNs);
@@ -261,8 +279,8 @@ lx_status launch_attn_paired(const CUtensorMap& mq, const CUtensorMap& mk, const
   // the two kept lists follow the tiles
   const size_t smem = 1024 + C::OFF_IDX + 2 * sizeof(int32_t) * (size_t)plan->k;
   if (smem > 227 * 1024) return LX_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(lx::sparse_attn_paired_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return cuda_failed();
+  const lx_status st = allow_most_shared<lx::sparse_attn_paired_kernel<D, true>>();
+  if (st != LX_OK) return st;
   lx::sparse_attn_paired_kernel<D, true><<<attn_grid(plan), 192, smem, s>>>(mq, mk, mv,
                                                                            attn_params<D>(plan, O, qs, ks, vs));
   return launch_status();
@@ -276,8 +294,8 @@ lx_status launch_attn(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   // the two kept lists and their K scales follow the tiles
   const size_t smem = 1024 + C::OFF_IDX + 16 * (size_t)plan->k;
   if (smem > 227 * 1024) return LX_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(lx::sparse_attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return cuda_failed();
+  const lx_status st = allow_most_shared<lx::sparse_attn_kernel<D, I8>>();
+  if (st != LX_OK) return st;
   lx::sparse_attn_kernel<D, I8><<<attn_grid(plan), C::THREADS, smem, s>>>(mq, mk, mv,
                                                                           attn_params<D>(plan, O, qs, ks, vs));
   return launch_status();
@@ -568,8 +586,8 @@ lx_status launch_gemv(lx::GemvArgs a, char* ws, cudaStream_t s) {
   if (OWN) tx = tw;   // not read
   if (!OWN && !make_map_codes(&tx, codes, (int64_t)P * a.M, a.K, P * a.M)) return LX_ERR_CUDA;
   const int smem = (int)(OWN ? lx::GemvOwnSmem::bytes(a.M, a.per) : lx::GemvSmem<P>::bytes(a.M));
-  if (cudaFuncSetAttribute(lx::nvfp4_gemv_kernel<P, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return cuda_failed();
+  const lx_status st = allow_most_shared<lx::nvfp4_gemv_kernel<P, OWN>>();
+  if (st != LX_OK) return st;
   // the kernels start while the work ahead of them ends (they wait for it themselves)
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -380,3 +380,78 @@ def test_few_long_prompts_are_split(lx, hq, hkv, D, lq, lk, causal):
                 r = oracle.packed_attn_ref(_np(Q)[h:h + 1, t:t + 1], _np(K)[g:g + 1, ck[i]:ck[i] + n],
                                            _np(V)[g:g + 1, ck[i]:ck[i] + n], [0, 1], [0, n], False, D ** -0.5)
                 _check(out[:, h:h + 1, t:t + 1], lse[h:h + 1, t:t + 1], r, D)
+
+
+# ---------------------------------------------------------------- rows computed again, in splits and for long
+def _hidden(lx, lq, lk, hq, hkv, D, bad, at, seed, prefix=0, key_too=True):
+    """A non-finite key and value at key `at` of the last sequence: rows that do not see it, and those that do."""
+    gen = torch.Generator().manual_seed(seed)
+    Q, K, V = _rows(gen, hq, sum(lq), D), _rows(gen, hkv, sum(lk), D), _rows(gen, hkv, sum(lk), D)
+    pre = [_rows(gen, hkv, prefix, D) for _ in range(2)] if prefix else []
+    cq, ck = _cu(lq), _cu(lk)
+    ref = oracle.packed_attn_ref(_np(Q), _np(K), _np(V), cq, ck, True, D ** -0.5, None, *[_np(t) for t in pre])
+    if key_too:
+        K[:, :, ck[-2] + at] = bad
+    V[:, :, ck[-2] + at] = bad
+    lse = torch.empty((hq, sum(lq)), device=DEV)
+    if prefix:
+        o = lx.lx_attn_prefix(Q, *pre, K, V, _i32(cq), _i32(ck), lse=lse)
+    else:
+        assert lx.lx_attn_packed_ws_size(Q, K, len(lq)) > 0
+        o = lx.lx_attn_packed(Q, K, V, _i32(cq), _i32(ck), lse=lse)
+    assert lx.lx_last_device_status() == 0
+    rows = np.ones((hq, sum(lq)), bool)
+    first = cq[-2] + max(0, at - (lk[-1] - lq[-1]))     # the first row that sees the key
+    rows[:, first:] = False
+    _check(o, lse, ref, D, rows)
+    if first < cq[-1]:
+        spoilt = o[:, :, first:].float()
+        if key_too or bad != bad:
+            assert torch.isnan(spoilt).all()
+        else:
+            assert (spoilt == bad).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("key_too", [True, False])
+@pytest.mark.parametrize("hq,hkv,D,lq,lk", [(2, 1, 64, [3, 9], [50, 5000]), (4, 2, 128, [9], [3000]),
+                                            (3, 1, 128, [2, 7], [300, 2600]), (6, 6, 64, [1, 40], [700, 4100])])
+def test_hidden_keys_do_not_enter_splits(lx, hq, hkv, D, lq, lk, bad, key_too):
+    """A few tokens over a cache whose keys are split: the key before the last one, and one in the middle of the rows."""
+    for back in (1, lq[-1] // 2):
+        _hidden(lx, lq, lk, hq, hkv, D, bad, lk[-1] - 1 - back, 40 + back, key_too=key_too)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("hq,hkv,D", [(1, 1, 64), (2, 2, 128)])
+def test_hidden_keys_do_not_enter_split_prompts(lx, hq, hkv, D, bad):
+    n = 2300
+    _hidden(lx, [n], [n], hq, hkv, D, bad, n - 30, 43, key_too=False)
+    _hidden(lx, [n], [n], hq, hkv, D, bad, 1200, 44)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("hq,hkv,D", [(2, 1, 64), (8, 2, 128), (3, 3, 128)])
+def test_hidden_keys_do_not_enter_behind_a_prefix(lx, hq, hkv, D, bad):
+    for key_too in (True, False):
+        _hidden(lx, [1, 9], [30, 9], hq, hkv, D, bad, 6, 45, prefix=300, key_too=key_too)
+        _hidden(lx, [4, 40], [4, 900], hq, hkv, D, bad, 870, 46, prefix=1500, key_too=key_too)
+
+
+def test_rows_computed_again_for_longer_than_a_wait(lx):
+    """A million tokens with a last value that is not finite: 127 rows are computed again, which takes a warp
+    longer than the 2 s that any wait of the others is limited to."""
+    n, D = 1 << 20, 64
+    gen = torch.Generator(device=DEV).manual_seed(47)
+    Q, K, V = (torch.randn((1, 1, n, D), device=DEV, generator=gen).to(torch.bfloat16) for _ in range(3))
+    V[:, :, n - 1] = float("inf")
+    lse = torch.empty((1, n), device=DEV)
+    cu = _i32([0, n])
+    assert lx.lx_attn_packed_ws_size(Q, K, 1) == 0
+    o = lx.lx_attn_packed(Q, K, V, cu, cu, lse=lse)
+    assert lx.lx_last_device_status() == 0
+    assert torch.isfinite(o[0, 0, :n - 1].float()).all() and (o[0, 0, n - 1] == float("inf")).all()
+    k, v = _np(K), _np(V)
+    for t in (n - 2, n - 65, n - 128, n - 129, n // 2):
+        r = oracle.packed_attn_ref(_np(Q)[:, t:t + 1], k[:, :t + 1], v[:, :t + 1], [0, 1], [0, t + 1], True, D ** -0.5)
+        _check(o[:, :, t:t + 1], lse[:, t:t + 1], r, D)

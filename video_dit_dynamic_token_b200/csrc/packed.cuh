@@ -436,12 +436,24 @@ __device__ __forceinline__ void st_global_32b(void* p, const uint32_t* x) {
                : "memory");
 }
 
+// As warp_wait, but the limit starts again while `beat` moves: rows that are computed again
+// (packed_exact_row) may take longer than any wait, and count their keys in it.
+__device__ __forceinline__ bool pack_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                          const volatile int* beat, uint64_t limit_ns) {
+  for (int seen = 0; !warp_wait(bar, parity, abort, limit_ns);) {
+    const int now = *beat;
+    if (!__any_sync(0xffffffffu, !*abort && now != seen)) return false;
+    seen = now;
+  }
+  return true;
+}
+
 // One row over keys [lo, hi), a warp together: lane holds D / 32 neighbouring
 // channels.  Returns the unnormalised row, its maximum (log2 domain) and sum.
 template <int D>
 __device__ __noinline__ void packed_exact_row(const __nv_bfloat16* q, const __nv_bfloat16* k, long long ksL,
                                               const __nv_bfloat16* v, long long vsL, int lo, int hi, float scale_log2,
-                                              float (&o)[D / 32], float& m, float& l) {
+                                              int* beat, float (&o)[D / 32], float& m, float& l) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float qf[E];
@@ -454,6 +466,7 @@ __device__ __noinline__ void packed_exact_row(const __nv_bfloat16* q, const __nv
   l = 0.f;
   constexpr int N = 4;   // keys at a time, whose loads and sums overlap
   for (int u = lo; u < hi; u += N) {
+    if (lane == 0 && ((u - lo) & 1023) == 0) atomicAdd(beat, 1);   // every millisecond at most
     float s[N], vf[N][E], mn = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -508,7 +521,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int busy[NQ][4];   // a warp is at its exponentials
   __shared__ volatile int abort_flag;
-  __shared__ int never_abort;
+  __shared__ int never_abort, beat;
   __shared__ PackTable table;
   __shared__ PackItem items[kPkItems];
 
@@ -534,6 +547,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     for (int g = 0; g < NQ; ++g) mbar_init(&bar_drain[g], 1);
     abort_flag = 0;
     never_abort = 0;
+    beat = 0;
     for (int i = 0; i < 8; ++i) busy[i >> 2][i & 3] = 0;
     fence_barrier_init();
   }
@@ -552,7 +566,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
 
   // the k-th item, for the warps that read items; done_item when it is not read any more
   auto next_item = [&](int k) {
-    return warp_wait(&bar_ifull[k % kPkItems], (uint32_t)(k / kPkItems) & 1u, &abort_flag, p.limit_ns);
+    return pack_wait(&bar_ifull[k % kPkItems], (uint32_t)(k / kPkItems) & 1u, &abort_flag, &beat, p.limit_ns);
   };
   auto done_item = [&](int k) {
     __syncwarp();
@@ -579,7 +593,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         PackItem it;
         pack_item(p, table, id, it);
         if (k >= kPkItems) {
-          ok = warp_wait(&bar_iempty[k % kPkItems], (uint32_t)(k / kPkItems - 1) & 1u, &abort_flag, p.limit_ns);
+          ok = pack_wait(&bar_iempty[k % kPkItems], (uint32_t)(k / kPkItems - 1) & 1u, &abort_flag, &beat, p.limit_ns);
           if (!ok) break;
         }
         if (leader) {
@@ -599,7 +613,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         for (int g = 0; g < NQ; ++g) {
           if (it.nt[g] == 0) continue;
           if (uq[g] > 0) {
-            ok = warp_wait(&bar_qempty[g], (uint32_t)(uq[g] - 1) & 1u, &abort_flag, p.limit_ns);
+            ok = pack_wait(&bar_qempty[g], (uint32_t)(uq[g] - 1) & 1u, &abort_flag, &beat, p.limit_ns);
             if (!ok) break;
           }
           if (leader) {
@@ -617,7 +631,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         auto load = [&](const CUtensorMap* map, int j, int g) {
           const int slot = m % C::RING;
           if (m >= C::RING &&
-              !warp_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, p.limit_ns))
+              !pack_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, &beat, p.limit_ns))
             return false;
           if (leader) {
             uint8_t* dst = sm + C::OFF_RING + slot * C::TILE_BYTES;
@@ -639,7 +653,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           }
         }
         if (!ok) break;
-        ok = warp_wait(&bar_clc, (uint32_t)k & 1u, &abort_flag, p.limit_ns);
+        ok = pack_wait(&bar_clc, (uint32_t)k & 1u, &abort_flag, &beat, p.limit_ns);
         if (!ok) break;
         asked = false;
         const int next = clc_answer(&clc);
@@ -679,7 +693,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       // slot, which a phase's parity does not show.
       int seen = 0;
       auto wait_load = [&](int at) {
-        return warp_wait(&bar_full[at % C::RING], (uint32_t)(at / C::RING) & 1u, &abort_flag, p.limit_ns);
+        return pack_wait(&bar_full[at % C::RING], (uint32_t)(at / C::RING) & 1u, &abort_flag, &beat, p.limit_ns);
       };
       auto skip_to = [&](int at) {   // loads of the other stream: nothing to do with them
         for (; seen < at; ++seen) {
@@ -709,7 +723,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           ok = skip_to(m);
           continue;
         }
-        ok = wait_full(at) && warp_wait(&bar_qfull[g], (uint32_t)(uq++) & 1u, &abort_flag, p.limit_ns);
+        ok = wait_full(at) && pack_wait(&bar_qfull[g], (uint32_t)(uq++) & 1u, &abort_flag, &beat, p.limit_ns);
         if (!ok) break;
         tc_fence_after();
         const int nt = (n + 1) / 2;
@@ -746,7 +760,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (b && 2 * j + 1 >= n) break;        // no visible key in the second half
-            ok = warp_wait(&bar_pfull[g][b], (uint32_t)(up[b]++) & 1u, &abort_flag, p.limit_ns);
+            ok = pack_wait(&bar_pfull[g][b], (uint32_t)(up[b]++) & 1u, &abort_flag, &beat, p.limit_ns);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -806,7 +820,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       float m_use = -INFINITY, l_run = 0.f, top;   // reference, sum, maximum of the tile
       const int whole = __reduce_min_sync(0xffffffffu, ahead);   // keys that all rows of the warp see
       for (int j = 0; j < my_nt; ++j) {
-        ok = warp_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, p.limit_ns);
+        ok = pack_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, &beat, p.limit_ns);
         if (!ok) break;
         const bool two = 2 * j + 1 < my_nh;
         if (!warp_live) {          // no rows: the scores only have to be handed back
@@ -922,7 +936,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         if (lane == 0) mbar_arrive(&bar_pfull[g][two ? 1 : 0]);
       }
       if (ok && my_nh > 0) {
-        ok = warp_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, p.limit_ns);
+        ok = pack_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, &beat, p.limit_ns);
         tc_fence_after();
       }
       if (ok && !warp_live) {
@@ -1013,7 +1027,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         if (!__any_sync(0xffffffffu, spoilt)) continue;
         float o[E], m, l;
         packed_exact_row<D>(p.q.p + s_head * p.q.sH + (long long)s_tr * p.q.sL, kb, p.k.sL, vb, p.v.sL, from, s_seen,
-                            sc, o, m, l);
+                            sc, &beat, o, m, l);
         const long long s_prow = slot * R + (long long)s_tr * (p.Hkv * p.G) + s_head;
 #pragma unroll
         for (int e = 0; e < E; ++e) {

@@ -436,16 +436,32 @@ __device__ __forceinline__ void st_global_32b(void* p, const uint32_t* x) {
                : "memory");
 }
 
-// As warp_wait, but the limit starts again while `beat` moves: rows that are computed again
-// (packed_exact_row) may take longer than any wait, and count their keys in it.
-__device__ __forceinline__ bool pack_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                          const volatile int* beat, uint64_t limit_ns) {
-  for (int seen = 0; !warp_wait(bar, parity, abort, limit_ns);) {
-    const int now = *beat;
-    if (!__any_sync(0xffffffffu, !*abort && now != seen)) return false;
-    seen = now;
+// As warp_wait, but the limit starts again while `state` moves: rows that are computed again
+// (packed_exact_row) may take longer than any wait, and count their keys in it, in twos; an odd
+// number ends all waits.  (One loop in the line: a second wait after the first one's limit made
+// all waits 3 % slower.)
+__device__ __forceinline__ bool pack_wait(uint64_t* bar, uint32_t parity, const volatile int* state, uint64_t limit_ns) {
+  bool ok = mbar_test_wait(bar, parity) || mbar_try_wait(bar, parity);
+  if (!ok) {
+    uint64_t t0 = globaltimer_ns();
+    int seen = 0;
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(bar, parity)) {
+        ok = true;
+        break;
+      }
+      if ((it & 63u) == 0u) {
+        const int now = *state;
+        if (now & 1) break;
+        if (globaltimer_ns() - t0 > limit_ns) {
+          if (now == seen) break;
+          seen = now;
+          t0 = globaltimer_ns();
+        }
+      }
+    }
   }
-  return true;
+  return __all_sync(0xffffffffu, ok);
 }
 
 // One row over keys [lo, hi), a warp together: lane holds D / 32 neighbouring
@@ -453,7 +469,7 @@ __device__ __forceinline__ bool pack_wait(uint64_t* bar, uint32_t parity, const 
 template <int D>
 __device__ __noinline__ void packed_exact_row(const __nv_bfloat16* q, const __nv_bfloat16* k, long long ksL,
                                               const __nv_bfloat16* v, long long vsL, int lo, int hi, float scale_log2,
-                                              int* beat, float (&o)[D / 32], float& m, float& l) {
+                                              int* state, float (&o)[D / 32], float& m, float& l) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float qf[E];
@@ -466,7 +482,7 @@ __device__ __noinline__ void packed_exact_row(const __nv_bfloat16* q, const __nv
   l = 0.f;
   constexpr int N = 4;   // keys at a time, whose loads and sums overlap
   for (int u = lo; u < hi; u += N) {
-    if (lane == 0 && ((u - lo) & 1023) == 0) atomicAdd(beat, 1);   // every millisecond at most
+    if (lane == 0 && ((u - lo) & 1023) == 0) atomicAdd(state, 2);   // every millisecond
     float s[N], vf[N][E], mn = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -520,8 +536,8 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
   __shared__ __align__(16) uint4 clc;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int busy[NQ][4];   // a warp is at its exponentials
-  __shared__ volatile int abort_flag;
-  __shared__ int never_abort, beat;
+  __shared__ volatile int abort_flag;    // odd: all waits end; else keys computed again (pack_wait)
+  __shared__ int never_abort;
   __shared__ PackTable table;
   __shared__ PackItem items[kPkItems];
 
@@ -547,7 +563,6 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     for (int g = 0; g < NQ; ++g) mbar_init(&bar_drain[g], 1);
     abort_flag = 0;
     never_abort = 0;
-    beat = 0;
     for (int i = 0; i < 8; ++i) busy[i >> 2][i & 3] = 0;
     fence_barrier_init();
   }
@@ -566,7 +581,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
 
   // the k-th item, for the warps that read items; done_item when it is not read any more
   auto next_item = [&](int k) {
-    return pack_wait(&bar_ifull[k % kPkItems], (uint32_t)(k / kPkItems) & 1u, &abort_flag, &beat, p.limit_ns);
+    return pack_wait(&bar_ifull[k % kPkItems], (uint32_t)(k / kPkItems) & 1u, &abort_flag, p.limit_ns);
   };
   auto done_item = [&](int k) {
     __syncwarp();
@@ -593,7 +608,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         PackItem it;
         pack_item(p, table, id, it);
         if (k >= kPkItems) {
-          ok = pack_wait(&bar_iempty[k % kPkItems], (uint32_t)(k / kPkItems - 1) & 1u, &abort_flag, &beat, p.limit_ns);
+          ok = pack_wait(&bar_iempty[k % kPkItems], (uint32_t)(k / kPkItems - 1) & 1u, &abort_flag, p.limit_ns);
           if (!ok) break;
         }
         if (leader) {
@@ -613,7 +628,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         for (int g = 0; g < NQ; ++g) {
           if (it.nt[g] == 0) continue;
           if (uq[g] > 0) {
-            ok = pack_wait(&bar_qempty[g], (uint32_t)(uq[g] - 1) & 1u, &abort_flag, &beat, p.limit_ns);
+            ok = pack_wait(&bar_qempty[g], (uint32_t)(uq[g] - 1) & 1u, &abort_flag, p.limit_ns);
             if (!ok) break;
           }
           if (leader) {
@@ -631,7 +646,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         auto load = [&](const CUtensorMap* map, int j, int g) {
           const int slot = m % C::RING;
           if (m >= C::RING &&
-              !pack_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, &beat, p.limit_ns))
+              !pack_wait(&bar_empty[slot], (uint32_t)((m / C::RING) - 1) & 1u, &abort_flag, p.limit_ns))
             return false;
           if (leader) {
             uint8_t* dst = sm + C::OFF_RING + slot * C::TILE_BYTES;
@@ -653,7 +668,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           }
         }
         if (!ok) break;
-        ok = pack_wait(&bar_clc, (uint32_t)k & 1u, &abort_flag, &beat, p.limit_ns);
+        ok = pack_wait(&bar_clc, (uint32_t)k & 1u, &abort_flag, p.limit_ns);
         if (!ok) break;
         asked = false;
         const int next = clc_answer(&clc);
@@ -693,7 +708,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       // slot, which a phase's parity does not show.
       int seen = 0;
       auto wait_load = [&](int at) {
-        return pack_wait(&bar_full[at % C::RING], (uint32_t)(at / C::RING) & 1u, &abort_flag, &beat, p.limit_ns);
+        return pack_wait(&bar_full[at % C::RING], (uint32_t)(at / C::RING) & 1u, &abort_flag, p.limit_ns);
       };
       auto skip_to = [&](int at) {   // loads of the other stream: nothing to do with them
         for (; seen < at; ++seen) {
@@ -723,7 +738,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
           ok = skip_to(m);
           continue;
         }
-        ok = wait_full(at) && pack_wait(&bar_qfull[g], (uint32_t)(uq++) & 1u, &abort_flag, &beat, p.limit_ns);
+        ok = wait_full(at) && pack_wait(&bar_qfull[g], (uint32_t)(uq++) & 1u, &abort_flag, p.limit_ns);
         if (!ok) break;
         tc_fence_after();
         const int nt = (n + 1) / 2;
@@ -760,7 +775,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (b && 2 * j + 1 >= n) break;        // no visible key in the second half
-            ok = pack_wait(&bar_pfull[g][b], (uint32_t)(up[b]++) & 1u, &abort_flag, &beat, p.limit_ns);
+            ok = pack_wait(&bar_pfull[g][b], (uint32_t)(up[b]++) & 1u, &abort_flag, p.limit_ns);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -820,7 +835,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       float m_use = -INFINITY, l_run = 0.f, top;   // reference, sum, maximum of the tile
       const int whole = __reduce_min_sync(0xffffffffu, ahead);   // keys that all rows of the warp see
       for (int j = 0; j < my_nt; ++j) {
-        ok = pack_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, &beat, p.limit_ns);
+        ok = pack_wait(&bar_sfull[g], (uint32_t)(us++) & 1u, &abort_flag, p.limit_ns);
         if (!ok) break;
         const bool two = 2 * j + 1 < my_nh;
         if (!warp_live) {          // no rows: the scores only have to be handed back
@@ -936,7 +951,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         if (lane == 0) mbar_arrive(&bar_pfull[g][two ? 1 : 0]);
       }
       if (ok && my_nh > 0) {
-        ok = pack_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, &beat, p.limit_ns);
+        ok = pack_wait(&bar_odone[g], (uint32_t)(uo++) & 1u, &abort_flag, p.limit_ns);
         tc_fence_after();
       }
       if (ok && !warp_live) {
@@ -1027,7 +1042,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         if (!__any_sync(0xffffffffu, spoilt)) continue;
         float o[E], m, l;
         packed_exact_row<D>(p.q.p + s_head * p.q.sH + (long long)s_tr * p.q.sL, kb, p.k.sL, vb, p.v.sL, from, s_seen,
-                            sc, &beat, o, m, l);
+                            sc, const_cast<int*>(&abort_flag), o, m, l);
         const long long s_prow = slot * R + (long long)s_tr * (p.Hkv * p.G) + s_head;
 #pragma unroll
         for (int e = 0; e < E; ++e) {

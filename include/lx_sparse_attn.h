@@ -319,8 +319,7 @@ typedef struct lx_pack {
 } lx_pack;
 
 /* Workspace of lx_attn_packed: 0 for prompts that give every SM two items or have at most
- * 2048 key rows, and for at most 256 key rows; else at most 64 MB, or two splits' worth for
- * many rows. */
+ * 2048 key rows, and for at most 256 key rows; else at most 64 MB and 4 bytes a sequence. */
 lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, size_t* bytes);
 
 /* Q, O [1, Hq, Tq, D]; K, V [1, Hkv, Tk, D], Hq a multiple of Hkv and at most 128
@@ -333,7 +332,7 @@ lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, 
 lx_status lx_attn_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, const lx_pack* pack, int causal,
                          float scale, const lx_bhld* O, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
-/* Workspace of lx_attn_prefix. */
+/* Workspace of lx_attn_prefix: at most 64 MB, or two splits' worth for many rows. */
 lx_status lx_attn_prefix_ws_size(const lx_bhld* Q, size_t* bytes);
 
 /* lx_attn_packed for a batch that shares a prefix: every row sees all keys of Kp, Vp

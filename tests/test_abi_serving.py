@@ -122,3 +122,18 @@ def test_gemv_refusals(lib):
     assert size(17, 320) == UNS and size(1, (1 << 24) + 64) == UNS and size(1, 64, (1 << 30) + 1) == UNS
     assert size(1, 100) == INV and size(0, 64) == INV and size(1, 64, 0) == INV
     assert lib.lx_nvfp4_gemv_ws_size(1, 64, 64, None) == INV
+
+
+def test_the_workspace_does_not_grow_with_the_rows(lib):
+    """Partial rows are kept for sequences that are split, in 64 MB at most: 200 prompts of 77 tokens."""
+    r, n = ctypes.byref, ctypes.c_size_t()
+    for rows, heads, seqs in ((77 * 24, 40, 24), (77 * 200, 40, 200), (100000, 40, 100000), (1 << 20, 64, 1 << 20)):
+        q = _view(H=heads, L=rows)
+        assert lib.lx_attn_packed_ws_size(r(q), r(q), seqs, r(n)) == 0
+        assert 0 < n.value <= (64 << 20) + 4 * seqs + 1024
+        pk = _pack(n=seqs)
+        assert _packed(lib, q=q, k=q, pk=pk, wb=n.value - 1) == WSP
+    # few rows: 128 splits of each, as many as a call can have, and a word for each sequence
+    q, k = _view(L=100), _view(H=2)
+    assert lib.lx_attn_packed_ws_size(r(q), r(k), 100, r(n)) == 0
+    assert n.value == 512 + 128 * 800 * (8 + 512)

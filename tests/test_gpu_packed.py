@@ -455,3 +455,59 @@ def test_rows_computed_again_for_longer_than_a_wait(lx):
     for t in (n - 2, n - 65, n - 128, n - 129, n // 2):
         r = oracle.packed_attn_ref(_np(Q)[:, t:t + 1], k[:, :t + 1], v[:, :t + 1], [0, 1], [0, t + 1], True, D ** -0.5)
         _check(o[:, :, t:t + 1], lse[:, t:t + 1], r, D)
+
+
+# ---------------------------------------------------------------- room for partial rows
+def _check_sampled(lx, lq, lk, hq, hkv, D, seqs, seed, heads=None, spare=3):
+    """A call whose K and V are made on the GPU, checked on whole sequences of some heads."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    mk = lambda T, H, f: ((torch.randn((T, H, D), device=DEV, generator=gen) * f).to(torch.bfloat16)
+                          .transpose(0, 1).unsqueeze(0))
+    cq, ck = _cu(lq), _cu(lk)
+    Q, K, V = mk(cq[-1] + spare, hq, 1.5), mk(ck[-1], hkv, 1.0), mk(ck[-1], hkv, 1.0)
+    out, lse = torch.full_like(Q, 7.0), torch.full((hq, Q.shape[2]), 9.0, device=DEV)
+    ws = torch.full((max(lx.lx_attn_packed_ws_size(Q, K, len(lq)), 256) + 256,), 255, dtype=torch.uint8, device=DEV)
+    lx.lx_attn_packed(Q, K, V, _i32(cq), _i32(ck), out=out, lse=lse, ws=ws[:-256])
+    assert lx.lx_last_device_status() == 0
+    assert torch.all(ws[-256:] == 255)
+    assert torch.all(out[:, :, cq[-1]:] == 7.0) and torch.all(lse[:, cq[-1]:] == 9.0)
+    for i in seqs:
+        a, b, c, d = cq[i], cq[i + 1], ck[i], ck[i + 1]
+        for h in (0, hq - 1) if heads is None else heads:
+            g = h // (hq // hkv)
+            r = oracle.packed_attn_ref(_np(Q[:, h:h + 1, a:b]), _np(K[:, g:g + 1, c:d]), _np(V[:, g:g + 1, c:d]),
+                                       [0, b - a], [0, d - c], True, D ** -0.5)
+            _check(out[:, h:h + 1, a:b], lse[h:h + 1, a:b], r, D)
+    return Q, K
+
+
+def test_many_short_prompts_need_little_room(lx):
+    """Prompts of at most a row tile each: nothing is split, and the workspace does not grow with the rows."""
+    Q, K = _check_sampled(lx, [77] * 200, [77] * 200, 40, 40, 128, (0, 99, 199), 50)
+    assert lx.lx_attn_packed_ws_size(Q, K, 200) <= (64 << 20) + 4096
+    _check_sampled(lx, [40, 77, 1, 128, 16] * 20, [40, 77, 1, 128, 16] * 20, 9, 3, 64, (0, 1, 2, 3, 99), 51)
+
+
+def test_splits_that_do_not_fit_get_longer(lx):
+    """More rows with splits than the workspace holds: 80 sequences of 32 tokens over 1,300 keys, eight over 2,600."""
+    lk = [2600 if i % 11 == 3 else 1300 for i in range(80)]
+    _check_sampled(lx, [32] * 80, lk, 32, 8, 128, (0, 3, 14, 79), 52)
+
+
+def test_heads_without_a_neighbour_are_not_split_where_there_is_no_room(lx):
+    """One key/value head, whose narrow items split their keys between two streams, and too many rows for that."""
+    lk = [130 + 7 * (i % 10) for i in range(2700)]
+    _check_sampled(lx, [1] * 2700, lk, 24, 1, 128, (0, 1, 1350, 2699), 53)
+    _check_sampled(lx, [1] * 700, lk[:700], 24, 1, 128, (0, 1, 350, 699), 54)
+
+
+def test_split_sequences_among_many(lx):
+    """A few long sequences among hundreds of short ones: each finds its own partial rows."""
+    r = np.random.default_rng(55)
+    lq = r.integers(0, 4, 900).tolist()
+    lk = r.integers(3, 60, 900).tolist()
+    long = (0, 5, 6, 130, 131, 501, 898, 899)
+    for i in long:
+        lq[i], lk[i] = 1 + i % 3, 2000 + 13 * i
+    _check_sampled(lx, lq, lk, 4, 2, 64, long + (1, 7, 132, 897), 56)
+    _check_sampled(lx, lq, lk, 6, 3, 64, long + (1, 7, 132, 897), 57)

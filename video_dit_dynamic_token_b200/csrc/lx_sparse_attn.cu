@@ -403,26 +403,27 @@ bool pack_fills(int64_t Tq, int64_t n, int64_t G, int64_t Hkv, int64_t Tk) {
   return pack_wide(Tq, n, G) && (Hkv * (Tq / (2 * pack_tokens(G))) >= 2 * lx::kPkSMs || Tk <= 16 * lx::kPkKeys);
 }
 
-// Room for partial rows: as many splits as 64 MB hold, 2 to 128 (behind a prefix
-// one of its own and one of the sequence's are the least); none where every
-// sequence is one split.
+// Room for partial rows, 64 MB or what 128 splits of every row take.  Without a prefix only the rows of sequences
+// that are split have any, and splits get longer where they would not fit (pack_prepare); no
+// workspace where every sequence is one split.  Behind a prefix every row has them: as many splits
+// as fit, at least one of the prefix and one of the sequence.
 struct PackWs {
-  int64_t splits;
-  size_t ml, part, total;   // [chunk | ml | part]
+  int64_t splits, room;            // with a prefix; without one: tokens
+  size_t start, ml, part, total;   // [chunk | start | ml | part]
 };
-PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D, int64_t Tk, bool prefix) {
+PackWs pack_layout(int64_t Tq, int64_t Hq, int64_t D, int64_t Tk, int64_t n, bool prefix) {
   PackWs w{};
   // no sequence is longer than two tiles: joining would cost more than it saves (three prompts
   // of 5 to 77 tokens 7.3 us, split 9.8)
-  if (!prefix && Tk <= 2 * lx::kPkKeys) {
-    w.splits = 1;
-    return w;
-  }
-  const int64_t R = Tq * Hq, row = 4 * D + 8;
-  w.splits = std::max<int64_t>(2, std::min<int64_t>(128, ((int64_t)64 << 20) / (R * row)));
-  w.ml = 256;
-  w.part = w.ml + align256((size_t)(w.splits * R * 8));
-  w.total = w.part + align256((size_t)(w.splits * R * D) * 4);
+  if (!prefix && Tk <= 2 * lx::kPkKeys) return w;
+  const int64_t R = Tq * Hq, row = 4 * D + 8, fit = ((int64_t)64 << 20) / row;
+  w.splits = std::max<int64_t>(2, std::min<int64_t>(128, fit / R));
+  w.room = std::min(128 * Tq, fit / Hq);
+  const int64_t rows = prefix ? w.splits * R : w.room * Hq;
+  w.start = 16;
+  w.ml = align256(w.start + (prefix ? 0 : sizeof(int) * (size_t)n));
+  w.part = w.ml + align256((size_t)(rows * 8));
+  w.total = w.part + align256((size_t)(rows * D) * 4);
   return w;
 }
 
@@ -491,20 +492,22 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   lx::PackParams p{};
   p.max_ns = 1;
   if (Kp || !pack_fills(Q->L, pack->n, G, K->H, K->L)) {
-    const PackWs w = pack_layout(Q->L, Q->H, Q->D, K->L, Kp != nullptr);
+    const PackWs w = pack_layout(Q->L, Q->H, Q->D, K->L, pack->n, Kp != nullptr);
     if (w.total) {
       if (!ws || ws_bytes < w.total) return LX_ERR_WORKSPACE;
       if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LX_ERR_ALIGN;
       char* base = reinterpret_cast<char*>(ws);
       p.chunk = reinterpret_cast<int*>(base);
+      p.start = reinterpret_cast<int*>(base + w.start);
       p.ml = reinterpret_cast<float2*>(base + w.ml);
       p.part = reinterpret_cast<float*>(base + w.part);
+      p.room = (int)w.room;
+      // no more splits than keys to split; behind a prefix shared out between it and the sequences
+      auto most = [](int64_t keys) { return std::max<int64_t>(1, (keys + lx::kPkKeys - 1) / lx::kPkKeys); };
+      const int64_t np = Kp ? std::min(w.splits / 2, most(Kp->L)) : 0;
+      p.max_ns = (int)std::min(Kp ? w.splits - np : 128, most(K->L));
+      p.max_np = Kp ? (int)(w.splits - p.max_ns) : 0;
     }
-    // shared out between the prefix and the sequences, but no more than keys to split
-    auto most = [](int64_t keys) { return std::max<int64_t>(1, (keys + lx::kPkKeys - 1) / lx::kPkKeys); };
-    const int64_t np = Kp ? std::min(w.splits / 2, most(Kp->L)) : 0;
-    p.max_ns = (int)std::min(w.splits - np, most(K->L));
-    p.max_np = Kp ? (int)(w.splits - p.max_ns) : 0;
   }
   p.cu_q = pack->cu_q;
   p.cu_k = pack->cu_k;
@@ -1048,7 +1051,7 @@ lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, 
   lx_status st;
   if ((st = check_packed(Q, K, K, Q)) != LX_OK) return st;
   if (!bytes || n < 1) return LX_ERR_INVALID;
-  *bytes = pack_fills(Q->L, n, Q->H / K->H, K->H, K->L) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, false).total;
+  *bytes = pack_fills(Q->L, n, Q->H / K->H, K->H, K->L) ? 0 : pack_layout(Q->L, Q->H, Q->D, K->L, n, false).total;
   return LX_OK;
 }
 
@@ -1061,7 +1064,7 @@ lx_status lx_attn_prefix_ws_size(const lx_bhld* Q, size_t* bytes) {
   lx_status st = check_bhld(Q);
   if (st != LX_OK) return st;
   if (!bytes || Q->B != 1) return LX_ERR_INVALID;
-  *bytes = pack_layout(Q->L, Q->H, Q->D, 0, true).total;
+  *bytes = pack_layout(Q->L, Q->H, Q->D, 0, 0, true).total;
   return LX_OK;
 }
 

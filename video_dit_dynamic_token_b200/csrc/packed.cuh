@@ -112,9 +112,13 @@ struct PackParams {
   long long osH, osL;
   int sectors;           // rows of o start at multiples of 32 bytes
   float* lse;            // [Hq][Tq] or null
-  float* part;           // [max_np + max_ns][Tq * Hq][D] unnormalised rows; null where nothing is split
-  float2* ml;            // [max_np + max_ns][Tq * Hq] (max, sum), max in the log2 domain
-  int* chunk;            // tiles per split, whether nothing is split; for the combine kernel
+  // Partial rows, [..][Hq] for each of `room` tokens: with a prefix [max_np + max_ns][Tq]; else
+  // [ns][lq] for each sequence that is split, one after the other.
+  float* part;           // [room][Hq][D] unnormalised rows; null where nothing is split
+  float2* ml;            // [room][Hq] (max, sum), max in the log2 domain
+  int* chunk;            // tiles per split, whether nothing is split, most splits; for the combine kernel
+  int* start;            // [n] first partial row of a sequence that is split, in tokens (no prefix)
+  int room;              // (no prefix)
   int max_np, max_ns;    // most splits of the prefix, of a sequence
   int wide;              // more than a row tile of tokens a sequence on average, no prefix
   int pair, units;       // key/value heads of a narrow item (1 or 2), Hkv / pair
@@ -181,6 +185,7 @@ struct PackItem {
   int slot[2];           // where a stream's partial result goes; -1: it finishes its rows; -2: no rows
   int head[2];           // key/value head of each stream
   int prefix;            // keys of the prefix (no causal rule)
+  int row0, step;        // partial row of token t (a row of Q) in slot x: row0 + x step + t
   int narrow;            // both streams have the item's rows, and a head or a range of keys each
   int stop;              // no further item
 };
@@ -193,16 +198,23 @@ struct PackTable {
   int longest;
   int c, np, pi;           // tiles per split, prefix splits, prefix items
   int total;               // items of a unit
+  int most;                // splits of a sequence
+  int need;                // partial rows of the sequences that are split, in tokens (no prefix)
   int before[kPkChunks + 1];
+  int rows[kPkChunks + 1];        // partial rows before each chunk (bits of an unsigned while they are added up)
 };
+constexpr int kPkManyRows = 1 << 18;   // more tokens than `room` holds; counts stop there
 
-// Splits and items of a sequence.
-__device__ __forceinline__ int pack_seq_splits(const PackParams& p, const PackSeq& s, int c) {
-  return pack_splits(p, s.lq, pack_tiles(s.lk), c, p.max_ns);
+// Splits and items of a sequence, and its partial rows in tokens (no prefix).
+__device__ __forceinline__ int pack_seq_splits(const PackParams& p, const PackSeq& s, int c, int most) {
+  return pack_splits(p, s.lq, pack_tiles(s.lk), c, most);
 }
-__device__ __forceinline__ int pack_seq_items(const PackParams& p, const PackSeq& s, int c) {
+__device__ __forceinline__ int pack_seq_items(const PackParams& p, const PackSeq& s, int ns) {
   if (p.Lp && s.lk == 0) return 0;   // behind a prefix a sequence may have no keys of its own
-  return pack_count(p, s.lq, pack_seq_splits(p, s, c));
+  return pack_count(p, s.lq, ns);
+}
+__device__ __forceinline__ int pack_seq_rows(const PackSeq& s, int ns) {
+  return ns == 1 ? 0 : (int)min((long long)s.lq * ns, (long long)kPkManyRows);
 }
 // Steps of a CTA over T key tiles for `rows` tokens of p.pair heads.
 __device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, int rows, int T) {
@@ -214,8 +226,12 @@ __device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, in
 template <int THREADS>
 __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   const int tid = threadIdx.x;
-  if (tid == 0) tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0, tb.c = 1 << 29;   // one split
-  for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0;
+  if (tid == 0) {
+    tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0;
+    tb.c = 1 << 29;   // one split
+    tb.most = p.max_ns;
+  }
+  for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
   const PackSeq mine = tid < p.n ? pack_seq(p, tid) : PackSeq{0, 0, 0, 0};   // read once where it covers the table
   __syncthreads();
   if (p.part) {
@@ -262,33 +278,57 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
         tb.np = pack_splits(p, rows, pt, c, p.max_np);
         tb.pi = pack_count(p, rows, tb.np);
       }
-      // by every CTA, all the same: which block numbers ever start is the launch control's affair
-      p.chunk[0] = c;
-      p.chunk[1] = p.wide && p.pair == 2 && c >= tb.longest;   // nothing to join
     }
     __syncthreads();
   }
-  const int cs = pack_div(p.n, kPkChunks), c = tb.c;
-  for (int i = tid; i < p.n; i += THREADS) {
-    const int m = pack_seq_items(p, i < THREADS ? mine : pack_seq(p, i), c);
-    if (m) atomicAdd(&tb.before[i / cs + 1], m);
-  }
-  __syncthreads();
-  if (tid < 32) {   // inclusive sums of 4 chunks a lane
-    int v[kPkChunks / 32], s = 0;
-#pragma unroll
-    for (int j = 0; j < kPkChunks / 32; ++j) v[j] = s += tb.before[1 + tid * (kPkChunks / 32) + j];
-    int run = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, run, o);
-      if (tid >= o) run += t;
+  const int cs = pack_div(p.n, kPkChunks);
+  const bool pool = p.part && !p.Lp;   // partial rows of split sequences only
+  for (;;) {
+    for (int i = tid; i < p.n; i += THREADS) {
+      const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
+      const int ns = pack_seq_splits(p, s, tb.c, tb.most), m = pack_seq_items(p, s, ns);
+      if (m) atomicAdd(&tb.before[i / cs + 1], m);
+      if (pool && ns > 1)   // 2^13 sequences in a chunk at most
+        atomicAdd(reinterpret_cast<unsigned*>(&tb.rows[i / cs + 1]), (unsigned)pack_seq_rows(s, ns));
     }
+    __syncthreads();
+    if (tid < 64) {   // inclusive sums of 4 chunks a lane: items by warp 0, partial rows by warp 1
+      const int lane = tid & 31, first = 1 + lane * (kPkChunks / 32);
+      int* sums = tid < 32 ? tb.before : tb.rows;
+      int v[kPkChunks / 32], s = 0;
 #pragma unroll
-    for (int j = 0; j < kPkChunks / 32; ++j) tb.before[1 + tid * (kPkChunks / 32) + j] = run - s + v[j];
-    if (tid == 31) tb.total = run + tb.pi;
+      for (int j = 0; j < kPkChunks / 32; ++j)
+        v[j] = s += tid < 32 ? sums[first + j] : (int)min((unsigned)sums[first + j], (unsigned)kPkManyRows);
+      int run = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += t;
+      }
+#pragma unroll
+      for (int j = 0; j < kPkChunks / 32; ++j) sums[first + j] = run - s + v[j];
+      if (tid == 31) tb.total = run + tb.pi;
+      if (tid == 63) tb.need = run;
+    }
+    __syncthreads();
+    if (tb.need <= p.room) break;
+    // More partial rows than there is room for: longer splits, at last none (then only heads without
+    // a neighbour are split, whose streams share the keys).
+    __syncthreads();
+    if (tid == 0) {
+      if (tb.c >= tb.longest) tb.most = 1;
+      const long long c = tb.c;
+      tb.c = (int)min((long long)tb.longest, max(c * tb.need / max(p.room, 1), c + c / 8 + 1));
+    }
+    for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
+    __syncthreads();
   }
-  __syncthreads();
+  if (tid == 0 && p.part) {
+    // by every CTA, all the same: which block numbers ever start is the launch control's affair
+    p.chunk[0] = tb.c;
+    p.chunk[1] = !p.Lp && tb.need == 0;   // nothing to join
+    p.chunk[2] = tb.most;
+  }
 }
 
 // Item number `id` (a warp together); stop past the last one.  In the order of a unit's
@@ -306,6 +346,8 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
   int x = id / turns;
   PackSeq s{0, 0, 0, 0};
   int ns, base = -1;                    // splits; slot of the first one
+  it.row0 = 0;
+  it.step = p.Tq;
   it.prefix = x < tb.pi;
   if (it.prefix) {
     s = pack_all(p);
@@ -318,11 +360,13 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
 #pragma unroll
     for (int j = 0; j < kPkChunks / 32; ++j) ch += __popc(__ballot_sync(0xffffffffu, tb.before[1 + j * 32 + lane] <= x));
     x -= tb.before[ch];
+    int rows = tb.rows[ch];        // partial rows before the sequence
     const int cs = pack_div(p.n, kPkChunks), end = min(p.n, (ch + 1) * cs);
+    int seq = 0;
     for (int b = ch * cs; b < end; b += 32) {
       const int i = b + lane;
       const PackSeq mine = i < end ? pack_seq(p, i) : PackSeq{0, 0, 0, 0};
-      const int m = pack_seq_items(p, mine, tb.c);
+      const int splits = pack_seq_splits(p, mine, tb.c, tb.most), m = pack_seq_items(p, mine, splits);
       int run = m;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -330,8 +374,10 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
         if (lane >= o) run += t;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, run > x);
+      const int src = hit ? __ffs(hit) - 1 : 32;
+      if (tb.need) rows += __reduce_add_sync(0xffffffffu, lane < src ? pack_seq_rows(mine, splits) : 0);
       if (hit) {
-        const int src = __ffs(hit) - 1;
+        seq = b + src;
         s.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
         s.lq = __shfl_sync(0xffffffffu, mine.lq, src);
         s.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
@@ -341,8 +387,13 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
       }
       x -= __shfl_sync(0xffffffffu, run, 31);
     }
-    ns = pack_seq_splits(p, s, tb.c);
+    ns = pack_seq_splits(p, s, tb.c, tb.most);
     if (p.Lp || ns > 1) base = tb.np;
+    if (!p.Lp && ns > 1) {
+      it.row0 = rows - s.q0;
+      it.step = s.lq;
+      if (lane == 0) p.start[seq] = rows;   // by each of its items, all the same
+    }
   }
   const int T = pack_tiles(s.lk), per = pack_div(T, ns), pairs = pack_pairs(p, s.lq);
   // first the pairs of row tiles, then the narrow rest; sequences are walked from the end,
@@ -964,7 +1015,9 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
       const int to = min(it.lk, from + my_nh * kPkHalf);
       const bool any = valid && seen > from && my_nh > 0;        // this row saw a key
       const long long tr = it.q0 + tok;
-      const long long R = (long long)p.Tq * p.Hkv * p.G, prow = slot * R + tr * (p.Hkv * p.G) + head;
+      // partial row of token t and query head h
+      auto part_row = [&](long long t, int h) { return ((long long)slot * it.step + it.row0 + t) * (p.Hkv * p.G) + h; };
+      const long long prow = part_row(tr, head);
       // rows without a key, rows with hidden keys: neither in most items
       const bool odd = !__all_sync(0xffffffffu, any || !valid) || __any_sync(0xffffffffu, any && seen < to);
       float check = 0.f;
@@ -1043,7 +1096,7 @@ __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
         float o[E], m, l;
         packed_exact_row<D>(p.q.p + s_head * p.q.sH + (long long)s_tr * p.q.sL, kb, p.k.sL, vb, p.v.sL, from, s_seen,
                             sc, const_cast<int*>(&abort_flag), o, m, l);
-        const long long s_prow = slot * R + (long long)s_tr * (p.Hkv * p.G) + s_head;
+        const long long s_prow = part_row(s_tr, s_head);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           if (slot < 0)
@@ -1082,7 +1135,9 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
   const long long R = (long long)p.Tq * Hq;
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");   // the partial rows are complete
   if (p.chunk[1]) return;
-  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < R; row += (long long)gridDim.x * 8) {
+  const int c = p.chunk[0], most = p.chunk[2];
+  const long long turn = (long long)gridDim.x * 8;
+  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < R; row += turn) {
     const int tok = (int)(row / Hq), head = (int)(row % Hq);
     // the last sequence that starts at or before this token
     int lo = 0, hi = p.n;
@@ -1094,6 +1149,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
       hi = min(hi, nl + step);
       lo = nl;
     }
+    const int start = p.Lp ? 0 : p.start[lo];   // (on its way with the lengths)
     const PackSeq s = pack_seq(p, lo);
     if (tok < s.q0 || tok >= s.q0 + s.lq) continue;
     int rows = 0;
@@ -1102,10 +1158,15 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
       if (tok < all.q0 || tok >= all.q0 + all.lq) continue;
       rows = all.lq;
     }
-    const int c = p.chunk[0];
     const int np = p.Lp ? pack_splits(p, rows, pack_tiles(p.Lp), c, p.max_np) : 0;
-    const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c);
-    if (!p.Lp && ns == 1) continue;   // its item finished the row
+    const int ns = (p.Lp && s.lk == 0) ? 0 : pack_seq_splits(p, s, c, most);
+    if (!p.Lp && ns == 1) {   // its items finished its rows: on to the first one behind them
+      row += ((long long)(s.q0 + s.lq) * Hq - 1 - row) / turn * turn;
+      continue;
+    }
+    // its partial rows, and how far apart the splits' are
+    const long long first = p.Lp ? row : (long long)(start + tok - s.q0) * Hq + head;
+    const long long apart = p.Lp ? R : (long long)s.lq * Hq;
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -1113,14 +1174,14 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
     // the maxima and sums (one after another: 10.8 us instead of 8.3 for 2,560 rows of 12 splits)
     for (int b = 0; b < np + ns; b += 32) {
       const int count = min(32, np + ns - b);
-      const long long base = (long long)b * R + row;
-      const float2 x = lane < count ? p.ml[base + lane * R] : make_float2(-INFINITY, 0.f);
+      const long long base = (long long)b * apart + first;
+      const float2 x = lane < count ? p.ml[base + lane * apart] : make_float2(-INFINITY, 0.f);
       float w = 0.f;
       for (int i = 0; i < count; i += 8) {
         float y[8][E];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const float* src = p.part + (base + (i + u) * R) * D + lane * E;
+          const float* src = p.part + (base + (i + u) * apart) * D + lane * E;
           if constexpr (E == 4) {
             const float4 z = i + u < count ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
             y[u][0] = z.x, y[u][1] = z.y, y[u][2] = z.z, y[u][3] = z.w;

@@ -318,8 +318,9 @@ typedef struct lx_pack {
   int64_t n;            /* sequences, 1 .. 2^20 */
 } lx_pack;
 
-/* Workspace of lx_attn_packed: 0 for prompts that give every SM two items or have at most
- * 2048 key rows, and for at most 256 key rows; else at most 64 MB and 4 bytes a sequence. */
+/* Workspace of lx_attn_packed: 0 for prompts that have at most 2048 key rows, or that give every
+ * SM two items and have at most 2048 key rows more than query rows, and for at most 256 key rows; else at
+ * most 64 MB and 4 bytes a sequence. */
 lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, size_t* bytes);
 
 /* Q, O [1, Hq, Tq, D]; K, V [1, Hkv, Tk, D], Hq a multiple of Hkv and at most 128

@@ -137,3 +137,12 @@ def test_the_workspace_does_not_grow_with_the_rows(lib):
     q, k = _view(L=100), _view(H=2)
     assert lib.lx_attn_packed_ws_size(r(q), r(k), 100, r(n)) == 0
     assert n.value == 512 + 128 * 800 * (8 + 512)
+
+
+def test_more_keys_than_rows_leave_the_split_to_the_lengths(lib):
+    """Prompts that fill the GPU need no workspace, unless a long cache may be among them."""
+    r, n = ctypes.byref, ctypes.c_size_t()
+    for keys, some in ((2112, False), (2112 + 2048, False), (2112 + 2049, True), (125000, True)):
+        q, k = _view(H=40, L=2112), _view(H=8, L=keys)
+        assert lib.lx_attn_packed_ws_size(r(q), r(k), 68, r(n)) == 0
+        assert (n.value > 0) == some

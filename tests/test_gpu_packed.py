@@ -511,3 +511,13 @@ def test_split_sequences_among_many(lx):
         lq[i], lk[i] = 1 + i % 3, 2000 + 13 * i
     _check_sampled(lx, lq, lk, 4, 2, 64, long + (1, 7, 132, 897), 56)
     _check_sampled(lx, lq, lk, 6, 3, 64, long + (1, 7, 132, 897), 57)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(40, 8, 128), (9, 3, 64)])
+def test_a_long_cache_among_prompts_is_split(lx, hq, hkv, D):
+    """Prompts that fill the GPU with single tokens in one call, one of them over a long cache."""
+    lq, lk = [500, 1, 700, 1, 1, 900] + [1] * 20, [500, 400, 700, 24000, 1, 900] + [300] * 20
+    if hkv == 3:
+        lq[2] = lk[2] = 5000
+    _check_sampled(lx, lq, lk, hq, hkv, D, (1, 3, 4, 25), 58, heads=(0, hq - 1))
+    _check_sampled(lx, lq, lk, hq, hkv, D, (0,), 58, heads=(1,))

@@ -397,10 +397,14 @@ inline int pack_tokens(int64_t G) { return (int)(128 / G); }
 // Prompts (more than a row tile of each sequence on average) that give every SM two items, or
 // whose keys are too few to split, gain nothing from it (the estimate in pack_prepare): such calls
 // need no workspace.  24 prompts of 17 to 2,000 tokens take 170 us whole, 255 split; 1,100 tokens
-// over 77 to 512 keys 15 and 27.
+// over 77 to 512 keys 15 and 27.  That is an average: where there are more keys than rows, a long cache may
+// be among them, and the lengths on the device decide (4 prompts of 512 tokens and 64 single tokens, one over
+// 60,000 keys, the others over 1,000: 1168 us whole, 137 split; all over 1,000: 77 without a workspace, 81).
 bool pack_wide(int64_t Tq, int64_t n, int64_t G) { return Tq > n * pack_tokens(G); }
 bool pack_fills(int64_t Tq, int64_t n, int64_t G, int64_t Hkv, int64_t Tk) {
-  return pack_wide(Tq, n, G) && (Hkv * (Tq / (2 * pack_tokens(G))) >= 2 * lx::kPkSMs || Tk <= 16 * lx::kPkKeys);
+  const int64_t few = 16 * lx::kPkKeys;
+  return pack_wide(Tq, n, G) &&
+         (Tk <= few || (Hkv * (Tq / (2 * pack_tokens(G))) >= 2 * lx::kPkSMs && Tk - Tq <= few));
 }
 
 // Room for partial rows, 64 MB or what 128 splits of every row take.  Without a prefix only the rows of sequences

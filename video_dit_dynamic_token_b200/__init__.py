@@ -387,9 +387,10 @@ def lx_sparse_attn(Q, K, V, keep, mode="int8fp8", plan: Plan | None = None, out=
 
 # ---------------------------------------------------------------- packed sequences
 # These calls serve single tokens, where marshalling counts: sizes of workspaces are
-# kept per shape, and the stream is asked for by device.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# kept per shape, and the stream is asked for by device.  (The public forms of the two functions take
+# longer; a torch build without CUDA has only them, and the sizes and checks work there too.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _with_stream(stream, t, call):

@@ -464,22 +464,6 @@ __device__ __forceinline__ void mma_f16_ts_lo(uint32_t d, uint32_t a, uint32_t b
       : "memory");
 }
 
-// 4 x 4 transposition of 16-byte pieces within each four lanes: lane i gives piece w
-// of its own and gets piece i of lane w's.
-__device__ __forceinline__ void transpose4(uint4 (&h)[4]) {
-  const int lane = threadIdx.x & 31;
-  auto swap = [&](uint4& a, uint4& b, int mask, bool up) {   // lanes with `up` give a and get b's place
-    const uint4 g = up ? a : b;
-    const uint4 r = make_uint4(__shfl_xor_sync(0xffffffffu, g.x, mask), __shfl_xor_sync(0xffffffffu, g.y, mask),
-                               __shfl_xor_sync(0xffffffffu, g.z, mask), __shfl_xor_sync(0xffffffffu, g.w, mask));
-    if (up) a = r; else b = r;
-  };
-  swap(h[0], h[1], 1, lane & 1);
-  swap(h[2], h[3], 1, lane & 1);
-  swap(h[0], h[2], 2, lane & 2);
-  swap(h[1], h[3], 2, lane & 2);
-}
-
 // 32 bytes, a whole sector (the address a multiple of 32).
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),

@@ -329,7 +329,8 @@ lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, 
  * aligned (may be NULL for size 0), not shared by calls that may overlap; O and lse
  * overlap none of the inputs.  The lengths are read on the device, so a captured call follows them.  A sequence
  * whose entries do not fit is left out and reported (LX_ERR_PLAN from
- * lx_last_device_status). */
+ * lx_last_device_status); so are all, where a table that descends counts rows more than once and
+ * makes more work than Q's rows have. */
 lx_status lx_attn_packed(const lx_bhld* Q, const lx_bhld* K, const lx_bhld* V, const lx_pack* pack, int causal,
                          float scale, const lx_bhld* O, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 

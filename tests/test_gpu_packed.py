@@ -521,3 +521,25 @@ def test_a_long_cache_among_prompts_is_split(lx, hq, hkv, D):
         lq[2] = lk[2] = 5000
     _check_sampled(lx, lq, lk, hq, hkv, D, (1, 3, 4, 25), 58, heads=(0, hq - 1))
     _check_sampled(lx, lq, lk, hq, hkv, D, (0,), 58, heads=(1,))
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+@pytest.mark.parametrize("hq,hkv,rows", [(4, 2, 8), (4, 2, 300), (3, 1, 40)])
+def test_a_table_that_counts_rows_again_and_again(lx, hq, hkv, rows, prefix):
+    """cu_q goes up and down: half the sequences own the same rows, with keys that would be split."""
+    from video_dit_dynamic_token_b200._abi import LX_ERR_PLAN
+    n, D, cap = 600, 64, 3000
+    gen = torch.Generator().manual_seed(59)
+    Q, K, V = _rows(gen, hq, rows + 4, D), _rows(gen, hkv, cap, D), _rows(gen, hkv, cap, D)
+    out, lse = torch.full_like(Q, 7.0), torch.full((hq, rows + 4), 9.0, device=DEV)
+    cq = _i32([0 if i % 2 == 0 else rows for i in range(n + 1)])
+    ck = _i32([0] + [cap] * n)
+    used = _i32([cap] + [0] * (n - 1))
+    for keys, lens in ((ck, None), (ck, used), (_i32([0 if i % 2 == 0 else cap for i in range(n + 1)]), None)):
+        a = (Q, K[:, :, :prefix], V[:, :, :prefix], K, V) if prefix else (Q, K, V)
+        call = lx.lx_attn_prefix if prefix else lx.lx_attn_packed
+        call(*a, cq, keys, len_k=lens, out=out, lse=lse)
+        assert lx.lx_last_device_status() == LX_ERR_PLAN
+        assert torch.all(out[:, :, rows:] == 7.0) and torch.all(lse[:, rows:] == 9.0)
+    good = lx.lx_attn_packed(Q, K, V, _i32([0, rows]), _i32([0, cap]))
+    assert lx.lx_last_device_status() == 0 and torch.isfinite(good[:, :, :rows].float()).all()

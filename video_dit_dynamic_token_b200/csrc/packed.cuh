@@ -131,7 +131,7 @@ struct PackSeq {
 };
 
 // Rows and keys of sequence i; a sequence whose entries do not fit the tensors is
-// reported and left out (lq = 0).
+// reported and left out (lq = 0, k0 = -1).
 __device__ __forceinline__ PackSeq pack_seq(const PackParams& p, int i) {
   const int a = p.cu_q[i], b = p.cu_q[i + 1], c = p.cu_k[i], d = p.cu_k[i + 1];
   PackSeq s{a, b - a, c, d - c};
@@ -143,7 +143,7 @@ __device__ __forceinline__ PackSeq pack_seq(const PackParams& p, int i) {
   }
   if (!ok) {
     report_error(-7);
-    s = PackSeq{0, 0, 0, 0};
+    s = PackSeq{0, 0, -1, 0};
   }
   return s;
 }
@@ -199,6 +199,7 @@ struct PackTable {
   int c, np, pi;           // tiles per split, prefix splits, prefix items
   int total;               // items of a unit
   int most;                // splits of a sequence
+  int bad;                 // a sequence was left out
   int need;                // partial rows of the sequences that are split, in tokens (no prefix)
   int before[kPkChunks + 1];
   int rows[kPkChunks + 1];        // partial rows before each chunk (bits of an unsigned while they are added up)
@@ -229,6 +230,7 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   if (tid == 0) {
     tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0;
     tb.c = 1 << 29;   // one split
+    tb.bad = 0;
     tb.most = p.max_ns;
   }
   for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
@@ -288,6 +290,7 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
       const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
       const int ns = pack_seq_splits(p, s, tb.c, tb.most), m = pack_seq_items(p, s, ns);
       if (m) atomicAdd(&tb.before[i / cs + 1], m);
+      if (s.k0 < 0) tb.bad = 1;
       if (pool && ns > 1)   // 2^13 sequences in a chunk at most
         atomicAdd(reinterpret_cast<unsigned*>(&tb.rows[i / cs + 1]), (unsigned)pack_seq_rows(s, ns));
     }
@@ -323,10 +326,25 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
     for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
     __syncthreads();
   }
+  if (tb.bad) {
+    // A table that descends may count rows more than once, and then has more items than the grid has
+    // blocks, or than 31 bits hold: none of them is worked on.
+    if (tid == 0) tb.work = 0;
+    __syncthreads();
+    unsigned long long all = 0;
+    for (int i = tid; i < p.n; i += THREADS) {
+      const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
+      all += pack_seq_items(p, s, pack_seq_splits(p, s, tb.c, tb.most));
+    }
+    if (all) atomicAdd(&tb.work, all);
+    __syncthreads();
+    if (tid == 0 && (tb.work + tb.pi) * p.units > gridDim.x) tb.total = tb.need = 0;
+    __syncthreads();
+  }
   if (tid == 0 && p.part) {
     // by every CTA, all the same: which block numbers ever start is the launch control's affair
     p.chunk[0] = tb.c;
-    p.chunk[1] = !p.Lp && tb.need == 0;   // nothing to join
+    p.chunk[1] = tb.total == 0 || (!p.Lp && tb.need == 0);   // nothing to join
     p.chunk[2] = tb.most;
   }
 }
@@ -1148,6 +1166,8 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackParams p)
       row += ((long long)(s.q0 + s.lq) * Hq - 1 - row) / turn * turn;
       continue;
     }
+    // (where a wait ran out, an item may not have said where its partial rows are)
+    if (!p.Lp && (start < 0 || start + (long long)s.lq * ns > p.room)) continue;
     // its partial rows, and how far apart the splits' are
     const long long first = p.Lp ? row : (long long)(start + tok - s.q0) * Hq + head;
     const long long apart = p.Lp ? R : (long long)s.lq * Hq;

@@ -324,8 +324,8 @@ typedef struct lx_pack {
 lx_status lx_attn_packed_ws_size(const lx_bhld* Q, const lx_bhld* K, int64_t n, size_t* bytes);
 
 /* Q, O [1, Hq, Tq, D]; K, V [1, Hkv, Tk, D], Hq a multiple of Hkv and at most 128
- * times it; any strides (e.g. the [T, H, D] layout of a projection); scale > 0 and
- * finite; lse fp32 [Hq, Tq] contiguous or NULL; ws of the size above, 256-byte
+ * times it; any strides (e.g. the [T, H, D] layout of a projection); scale > 0, and
+ * scale log2(e) finite in fp32; lse fp32 [Hq, Tq] contiguous or NULL; ws of the size above, 256-byte
  * aligned (may be NULL for size 0), not shared by calls that may overlap; O and lse
  * overlap none of the inputs.  The lengths are read on the device, so a captured call follows them.  A sequence
  * whose entries do not fit is left out and reported (LX_ERR_PLAN from

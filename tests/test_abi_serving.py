@@ -146,3 +146,9 @@ def test_more_keys_than_rows_leave_the_split_to_the_lengths(lib):
         q, k = _view(H=40, L=2112), _view(H=8, L=keys)
         assert lib.lx_attn_packed_ws_size(r(q), r(k), 68, r(n)) == 0
         assert (n.value > 0) == some
+
+
+def test_a_scale_whose_exponent_overflows(lib):
+    """scale * log2(e), which the kernels work with, has to be finite: 0 * inf would be NaN."""
+    assert _packed(lib, scale=2.4e38) == INV and _packed(lib, scale=3.4e38) == INV
+    assert _packed(lib, scale=2.3e38, k=_view(H=2, L=3000), ws=None) == WSP       # the check after it

@@ -488,7 +488,8 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   if (st != LX_OK) return st;
   if (!pack || !pack->cu_q || !pack->cu_k || pack->n < 1) return LX_ERR_INVALID;
   if (pack->n > (int64_t)1 << 20) return LX_ERR_UNSUPPORTED;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return LX_ERR_INVALID;
+  const float scale_log2 = (float)(1.4426950408889634 * (double)scale);   // what the kernels work with
+  if (!(scale > 0.f) || !std::isfinite(scale_log2)) return LX_ERR_INVALID;
   if ((reinterpret_cast<uintptr_t>(pack->cu_q) | reinterpret_cast<uintptr_t>(pack->cu_k) |
        reinterpret_cast<uintptr_t>(pack->len_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
     return LX_ERR_ALIGN;
@@ -525,7 +526,7 @@ lx_status attn_packed_impl(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* V
   p.TQ = pack_tokens(G);
   p.causal = causal != 0;
   p.wide = !Kp && pack_wide(Q->L, pack->n, G);
-  p.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  p.scale_log2 = scale_log2;
   p.pair = K->H % 2 == 0 ? 2 : 1;
   p.units = (int)(K->H / p.pair);
   // units at a time: as many as keep K and V within half of the 126 MB L2, in even groups

@@ -567,8 +567,10 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
     N, codes, sf, gw = wq.R, wq.codes, wq.sf, wq.gscale
     if K != wq.K:
         raise ValueError("x and W differ in K")
-    if codes.numel() * 2 != N * K or sf.numel() < (N + 127) // 128 * 8 * K:
-        raise ValueError("W: not the codes and scales of an [N, K] tensor")
+    if (codes.numel() * 2 != N * K or sf.numel() < (N + 127) // 128 * 8 * K or codes.element_size() != 1
+            or sf.element_size() != 1 or not codes.is_contiguous() or not sf.is_contiguous()
+            or gw.dtype is not torch.float32 or gw.numel() != 1):
+        raise ValueError("W: not the codes, scales and global scale of an [N, K] tensor")
     if bias is not None and (bias.dtype is not torch.float32 or not bias.is_contiguous() or bias.numel() != N):
         raise ValueError("bias must be a contiguous fp32 tensor of N elements")
     dev = _same_device((x, codes, sf, gw), (bias, out, ws))

@@ -403,7 +403,7 @@ lx_status lx_nvfp4_gemv_ws_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
  * W = (wc, wsf, gw) [N, K] as written by lx_nvfp4_quantize, N at most 2^30, K % 64 == 0
  * and at most 2^24; bias fp32 [N] or NULL; y bf16 [M, N], row stride ldy >= N.  x, wc, wsf
  * 16-byte aligned; ws of the size above, 256-byte aligned (may be NULL for size 0), not
- * shared by calls that may overlap.  More rows are LX_ERR_UNSUPPORTED: lx_nvfp4_gemm is the form for them. */
+ * shared by calls that may overlap; y overlaps none of the inputs.  More rows are LX_ERR_UNSUPPORTED: lx_nvfp4_gemm is the form for them. */
 lx_status lx_nvfp4_gemv(const void* x, int64_t M, int64_t ldx, const uint8_t* wc, const uint8_t* wsf, const float* gw,
                         const float* bias, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, size_t ws_bytes,
                         cudaStream_t stream);

@@ -256,3 +256,21 @@ def test_many_turns_of_the_ring(lx, M):
         assert torch.equal(y, first)
     torch.cuda.synchronize()
     assert lx.lx_last_device_status() == 0
+
+
+def test_one_row_of_any_stride(lx):
+    """A single row has no row stride: views whose stride is no multiple of 8, smaller than K or N, or zero."""
+    rng = np.random.default_rng(8)
+    N, K = 150, 320
+    wq, wr = _weights(lx, rng, N, K)
+    data = _bf16(rng.standard_normal(K))
+    want = _check(lx, data[None], wq, wr)
+    buf = torch.zeros(1024, dtype=torch.bfloat16, device=DEV)
+    for stride in (0, 1, 321, 325):
+        x = torch.as_strided(data, (1, K), (stride, 1))
+        out = torch.as_strided(buf, (1, N), (stride, 1))
+        buf.zero_()
+        assert torch.equal(lx.lx_nvfp4_gemv(x, wq), want)
+        lx.lx_nvfp4_gemv(x, wq, out=out)
+        assert torch.equal(out, want) and not buf[N:].any()
+    assert lx.lx_last_device_status() == 0

@@ -557,7 +557,9 @@ def lx_nvfp4_gemv_ws_size(M, N, K) -> int:
 
 
 def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None):
-    """Y = x W^T + bias in bf16 [M, N] for M <= 16 bf16 rows x [M, K] and NVFP4 W [N, K]; bias fp32 [N] or None."""
+    """Y = x W^T + bias in bf16 [M, N] for M <= 16 bf16 rows x [M, K] and NVFP4 W [N, K]; bias fp32 [N] or None.
+
+    `out` overlaps neither x nor the weights."""
     if stream is not None:
         return _with_stream(stream, x, lambda: lx_nvfp4_gemv(x, wq, bias, out, ws))
     strides = x.stride()
@@ -581,7 +583,7 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
         out = x.new_empty((M, N))
         ldy = N
     elif out.dtype is torch.bfloat16 and out.shape == (M, N) and out.stride(1) == 1:
-        ldy = out.stride(0) if M > 1 else max(out.stride(0), N)
+        ldy = out.stride(0) if M > 1 else N
     else:
         raise ValueError("out must be a bf16 [M, N] tensor with contiguous rows")
     if ws is None:
@@ -589,7 +591,7 @@ def lx_nvfp4_gemv(x, wq: NvFp4Tensor, bias=None, out=None, ws=None, stream=None)
         if size:
             ws = x.new_empty(size, dtype=torch.uint8)
     status = _abi.load().lx_nvfp4_gemv(
-        x.data_ptr(), M, strides[0] if M > 1 else max(strides[0], K), codes.data_ptr(), sf.data_ptr(), gw.data_ptr(),
+        x.data_ptr(), M, strides[0] if M > 1 else K, codes.data_ptr(), sf.data_ptr(), gw.data_ptr(),
         None if bias is None else bias.data_ptr(), N, K, out.data_ptr(), ldy,
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(dev))
     if status:

@@ -223,6 +223,76 @@ __device__ __forceinline__ unsigned long long pack_steps(const PackParams& p, in
          pack_narrow(p, rows) * (p.pair == 2 ? T : (T + 1) / 2);
 }
 
+// Items and partial rows of all sequences for splits of tb.c tiles, and their sums; before and rows are zero.
+// seq(i): sequence i.
+template <int THREADS, class Seq>
+__device__ __forceinline__ void pack_count_all(const PackParams& p, PackTable& tb, const Seq& seq) {
+  const int tid = threadIdx.x, cs = pack_div(p.n, kPkChunks);
+  const bool pool = p.part && !p.Lp;   // partial rows of split sequences only
+  for (int i = tid; i < p.n; i += THREADS) {
+    const PackSeq s = seq(i);
+    const int ns = pack_seq_splits(p, s, tb.c, tb.most), m = pack_seq_items(p, s, ns);
+    if (m) atomicAdd(&tb.before[i / cs + 1], m);
+    if (s.k0 < 0) tb.bad = 1;
+    if (pool && ns > 1)   // 2^13 sequences in a chunk at most
+      atomicAdd(reinterpret_cast<unsigned*>(&tb.rows[i / cs + 1]), (unsigned)pack_seq_rows(s, ns));
+  }
+  __syncthreads();
+  if (tid < (pool ? 64 : 32)) {   // inclusive sums of 4 chunks a lane: items by warp 0, partial rows by warp 1
+    const int lane = tid & 31, first = 1 + lane * (kPkChunks / 32);
+    int* sums = tid < 32 ? tb.before : tb.rows;
+    int v[kPkChunks / 32], s = 0;
+#pragma unroll
+    for (int j = 0; j < kPkChunks / 32; ++j)
+      v[j] = s += tid < 32 ? sums[first + j] : (int)min((unsigned)sums[first + j], (unsigned)kPkManyRows);
+    int run = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += t;
+    }
+#pragma unroll
+    for (int j = 0; j < kPkChunks / 32; ++j) sums[first + j] = run - s + v[j];
+    if (tid == 31) tb.total = run + tb.pi;
+    if (tid == 63) tb.need = run;
+  }
+  __syncthreads();
+}
+
+// What few calls need, out of the line (in it, it cost the smallest calls 0.5 us):
+// - More partial rows than there is room for: longer splits, at last none (then only heads without a
+//   neighbour are split, whose streams share the keys).
+// - A table that descends may count rows more than once, and then has more items than the grid has
+//   blocks, or than 31 bits hold: none of them is worked on.
+template <int THREADS>
+__device__ __noinline__ void pack_refit(const PackParams& p, PackTable& tb) {
+  const int tid = threadIdx.x;
+  auto seq = [&](int i) { return pack_seq(p, i); };
+  while (tb.need > p.room) {
+    __syncthreads();
+    if (tid == 0) {
+      if (tb.c >= tb.longest) tb.most = 1;
+      const long long c = tb.c;
+      tb.c = (int)min((long long)tb.longest, max(c * tb.need / max(p.room, 1), c + c / 8 + 1));
+    }
+    for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
+    __syncthreads();
+    pack_count_all<THREADS>(p, tb, seq);
+  }
+  if (!tb.bad) return;
+  if (tid == 0) tb.work = 0;
+  __syncthreads();
+  unsigned long long all = 0;
+  for (int i = tid; i < p.n; i += THREADS) {
+    const PackSeq s = pack_seq(p, i);
+    all += pack_seq_items(p, s, pack_seq_splits(p, s, tb.c, tb.most));
+  }
+  if (all) atomicAdd(&tb.work, all);
+  __syncthreads();
+  if (tid == 0 && (tb.work + tb.pi) * p.units > gridDim.x) tb.total = tb.need = 0;
+  __syncthreads();
+}
+
 // Every thread reads a share of the table, so that lengths stay on the device.
 template <int THREADS>
 __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
@@ -230,7 +300,7 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
   if (tid == 0) {
     tb.work = 0, tb.hidden = 0, tb.longest = 0, tb.np = 0, tb.pi = 0;
     tb.c = 1 << 29;   // one split
-    tb.bad = 0;
+    tb.bad = tb.need = 0;
     tb.most = p.max_ns;
   }
   for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
@@ -283,64 +353,8 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
     }
     __syncthreads();
   }
-  const int cs = pack_div(p.n, kPkChunks);
-  const bool pool = p.part && !p.Lp;   // partial rows of split sequences only
-  for (;;) {
-    for (int i = tid; i < p.n; i += THREADS) {
-      const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
-      const int ns = pack_seq_splits(p, s, tb.c, tb.most), m = pack_seq_items(p, s, ns);
-      if (m) atomicAdd(&tb.before[i / cs + 1], m);
-      if (s.k0 < 0) tb.bad = 1;
-      if (pool && ns > 1)   // 2^13 sequences in a chunk at most
-        atomicAdd(reinterpret_cast<unsigned*>(&tb.rows[i / cs + 1]), (unsigned)pack_seq_rows(s, ns));
-    }
-    __syncthreads();
-    if (tid < 64) {   // inclusive sums of 4 chunks a lane: items by warp 0, partial rows by warp 1
-      const int lane = tid & 31, first = 1 + lane * (kPkChunks / 32);
-      int* sums = tid < 32 ? tb.before : tb.rows;
-      int v[kPkChunks / 32], s = 0;
-#pragma unroll
-      for (int j = 0; j < kPkChunks / 32; ++j)
-        v[j] = s += tid < 32 ? sums[first + j] : (int)min((unsigned)sums[first + j], (unsigned)kPkManyRows);
-      int run = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += t;
-      }
-#pragma unroll
-      for (int j = 0; j < kPkChunks / 32; ++j) sums[first + j] = run - s + v[j];
-      if (tid == 31) tb.total = run + tb.pi;
-      if (tid == 63) tb.need = run;
-    }
-    __syncthreads();
-    if (tb.need <= p.room) break;
-    // More partial rows than there is room for: longer splits, at last none (then only heads without
-    // a neighbour are split, whose streams share the keys).
-    __syncthreads();
-    if (tid == 0) {
-      if (tb.c >= tb.longest) tb.most = 1;
-      const long long c = tb.c;
-      tb.c = (int)min((long long)tb.longest, max(c * tb.need / max(p.room, 1), c + c / 8 + 1));
-    }
-    for (int i = tid; i <= kPkChunks; i += THREADS) tb.before[i] = 0, tb.rows[i] = 0;
-    __syncthreads();
-  }
-  if (tb.bad) {
-    // A table that descends may count rows more than once, and then has more items than the grid has
-    // blocks, or than 31 bits hold: none of them is worked on.
-    if (tid == 0) tb.work = 0;
-    __syncthreads();
-    unsigned long long all = 0;
-    for (int i = tid; i < p.n; i += THREADS) {
-      const PackSeq s = i < THREADS ? mine : pack_seq(p, i);
-      all += pack_seq_items(p, s, pack_seq_splits(p, s, tb.c, tb.most));
-    }
-    if (all) atomicAdd(&tb.work, all);
-    __syncthreads();
-    if (tid == 0 && (tb.work + tb.pi) * p.units > gridDim.x) tb.total = tb.need = 0;
-    __syncthreads();
-  }
+  pack_count_all<THREADS>(p, tb, [&](int i) { return i < THREADS ? mine : pack_seq(p, i); });
+  if (tb.bad || tb.need > p.room) pack_refit<THREADS>(p, tb);
   if (tid == 0 && p.part) {
     // by every CTA, all the same: which block numbers ever start is the launch control's affair
     p.chunk[0] = tb.c;
@@ -378,7 +392,7 @@ __device__ __forceinline__ void pack_item(const PackParams& p, const PackTable& 
 #pragma unroll
     for (int j = 0; j < kPkChunks / 32; ++j) ch += __popc(__ballot_sync(0xffffffffu, tb.before[1 + j * 32 + lane] <= x));
     x -= tb.before[ch];
-    int rows = tb.rows[ch];        // partial rows before the sequence
+    int rows = tb.need ? tb.rows[ch] : 0;   // partial rows before the sequence
     const int cs = pack_div(p.n, kPkChunks), end = min(p.n, (ch + 1) * cs);
     int seq = 0;
     for (int b = ch * cs; b < end; b += 32) {
@@ -577,7 +591,7 @@ template <int D>
 __global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
     packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKp,
-                       const __grid_constant__ CUtensorMap tmVp, const PackParams p) {
+                       const __grid_constant__ CUtensorMap tmVp, const __grid_constant__ PackParams p) {
   using C = PackCfg<D>;
   constexpr int NQ = 2;   // streams
   extern __shared__ __align__(1024) uint8_t smem_raw[];

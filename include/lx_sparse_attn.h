@@ -340,7 +340,8 @@ lx_status lx_attn_prefix_ws_size(const lx_bhld* Q, size_t* bytes);
 /* lx_attn_packed for a batch that shares a prefix: every row sees all keys of Kp, Vp
  * [1, Hkv, Lp, D] before those of its own sequence.  The prefix is read once for
  * all sequences; the two parts of a row are joined in fp32.  A sequence may have
- * no keys of its own. */
+ * no keys of its own.  For few rows a sequence: prompts of hundreds of rows are quicker, and need less
+ * workspace, as one packed call over copies of the prefix (8 x 2,000 rows behind 1,000 keys: 1,213 and 592 us). */
 lx_status lx_attn_prefix(const lx_bhld* Q, const lx_bhld* Kp, const lx_bhld* Vp, const lx_bhld* K, const lx_bhld* V,
                          const lx_pack* pack, int causal, float scale, const lx_bhld* O, float* lse, void* ws,
                          size_t ws_bytes, cudaStream_t stream);

@@ -7,7 +7,7 @@
 // bytes of codes and N K / 16 of scales, which is what bounds large ones (30720 x 5120, cold:
 // one row 21.5 us = 4.1 TB/s, 120 of the 148 SMs having a tile; 8 and 16 rows 23.3).
 // Small ones are bound by the start, the digits and the joining of sums (5120 x 5120, two
-// rows: 8.6 us; 256 x 512, one row: 5.9).
+// rows: 8.6 us with the weights in the L2 cache, 11.0 without; 256 x 512, one row: 5.9).
 //
 // Decoding 4-bit weights costs more issue slots than an SM has at the rate they
 // arrive (42 weights per clock; mma.sync on weights decoded to fp16 took 38 to 55 us
@@ -61,9 +61,11 @@ constexpr int kGvMaxStages = 5;
 // Up to this many elements of x, and up to this many weights, the product kernel writes the
 // digits itself, each CTA those of its range of K (8 bytes of shared memory an element): one
 // launch and no workspace, 4 us less of the host's time, which such calls wait for (two rows x
-// 5120 x 5120: 8.6 us on the device instead of 8.4).  Beyond, and for more than 8 rows, they
+// 5120 x 5120: 8.6 us on the device instead of 8.4; 0.7 more for 8 x 1280).  Beyond, and for more than 8 rows, they
 // come from a pass of their own, as every CTA would read all of x and write its part again (two
-// rows x 30720 x 5120: 24.3 us, with the pass 21.6).
+// rows x 30720 x 5120: 24.3 us, with the pass 21.6).  On the device and with the host, own digits and the
+// pass, by elements of x: 10240 (8 x 1280) 7.9 and 8.2, 7.3 and 10.0; 12800 (5 x 2560) 9.2 and 9.4, 7.6
+// and 10.1; 13824 (one row) 11.1 and 11.1, 10.9 and 11.1; 15360 (3 x 5120) 11.2 and 11.2, 9.7 and 10.2.
 constexpr int kGvOwnDigits = 10240;
 constexpr long long kGvOwnWeights = 1 << 25;
 constexpr uint32_t kGvSmemLimit = 227 * 1024 - 2048;

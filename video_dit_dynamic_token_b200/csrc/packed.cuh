@@ -22,7 +22,8 @@
 // for an odd number, the last one half empty: 39 instead of 31 us with one head.)
 // Key ranges (splits) also spread long sequences over the SMs when there are few items:
 // a split leaves its unnormalised fp32 rows and (max, sum), and packed_combine_kernel
-// joins them.  A row whose keys are one split is finished by its item.
+// joins them.  A row whose keys are one split is finished by its item, and only sequences that are
+// split have partial rows (200 prompts of 77 tokens, 40 heads: 368 us with a place for every row, 212).
 //
 // One CTA per SM.  The grid has a block for every item there can be; a running CTA takes
 // over blocks that have not started (cluster launch control), so that items are
@@ -54,12 +55,13 @@
 // past a sequence's end are zeroed in shared memory before they are used.  A
 // key that the causal rule hides from some rows of a tile and not from others
 // has P = 0 there, and 0 * V is NaN when V is not finite: a row that ends
-// non-finite and has such keys is computed again by packed_exact_row.
+// non-finite and has such keys is computed again by packed_exact_row (up to 32 rows a warp, one after
+// another: 0.4 s for a sequence of 75,600 keys, 8.5 s for a million; other waits go on meanwhile).
 //
 // Measured (D = 128, in a graph, inputs colder than L2): a causal sequence of 32,760 tokens with
-// 40 heads 10.0 to 10.4 ms (1.1 PFLOP/s); 16,000 video tokens over prompts of 77 to 512 keys 134 us
-// (2.5 TB/s); one token in each of 48 sequences of 200 to 8,000 keys, 40 heads on 8, 107 us
-// (4.3 TB/s); 64 tokens behind 8,192 shared keys 46 us.
+// 40 heads 10.0 to 10.4 ms (1.1 PFLOP/s); 16,000 video tokens over prompts of 77 to 512 keys 134 to 140 us
+// (2.5 TB/s); one token in each of 48 sequences of 200 to 8,000 keys, 40 heads on 8, 106 us
+// (4.4 TB/s); 64 tokens behind 8,192 shared keys 46 us; three prompts of 5 to 77 tokens 7.8.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -340,7 +342,10 @@ __device__ void pack_prepare(const PackParams& p, PackTable& tb) {
       // Row tiles full of tokens pay for a split with their partial rows, about as much as 7
       // tiles.  Times in tiles, fitted to single prompts of 2,000 to 16,128 tokens with 1 to 10
       // heads (split, whole; 1.9 us a tile): 10 heads x 4,000 103, 66 us; 10 x 2,000 51, 36;
-      // 2 x 16,128 210, 223; 1 x 8,000 52, 118.
+      // 2 x 16,128 210, 223; 1 x 8,000 52, 118.  With D = 64 (split, whole): 10 x 4,000 93, 64;
+      // 10 x 2,300 50, 41; 2 x 16,128 198, 225; 1 x 8,000 45, 113; 12 x 8,000 265, 184.  The estimate is too
+      // high for few short items, with either D: 2 x 2,300 stay whole, 40 us instead of 23 (D = 128: 42, 26),
+      // and so do 2 x 8,000 without the causal rule, 119 instead of 76 (126, 89).
       if (p.wide) {
         const long long C = (long long)((work - tb.hidden * p.units + kPkSMs - 1) / kPkSMs), l = tb.longest;
         if (max(l, C + l / 2) <= C + C / 2 + 7 * ((C + c - 1) / c) + 8) c = max(1, tb.longest);

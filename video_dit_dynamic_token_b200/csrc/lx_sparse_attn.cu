@@ -139,11 +139,12 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, const c
   for (int i = 0; i < N; ++i) es[i] = 1;
   auto encode = [&]() {
     return fn(m, dt, N, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
-  if (encode()) return true;
+  const CUresult r = encode();
+  if (r != CUDA_ERROR_INVALID_CONTEXT && r != CUDA_ERROR_NOT_INITIALIZED) return r == CUDA_SUCCESS;
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode() == CUDA_SUCCESS;
 }
 
 // 4-D map over [B,H,L,D] (innermost first: D, L, H, B), strides in elements.
